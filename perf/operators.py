@@ -29,7 +29,8 @@ own = False
 
 PAGE = 16
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
-MIN_EXP = {"f16": -23, "bf16": -120}  # smallest block exponent: half of 2^e stays representable
+# Smallest and largest block exponent: every value stays exact in the 16-bit type.
+EXP = {"f16": (-23, 13), "bf16": (-120, 125)}
 
 
 # ---- cases -------------------------------------------------------------------
@@ -195,7 +196,8 @@ def _quantise(x, dtype):
     top = x.abs().amax(-1)
     fine = torch.isfinite(x).all(-1)
     mant, exp = torch.frexp(torch.where(fine, top, 0))
-    e = torch.where(top == 0, MIN_EXP[dtype], exp - 3 + (mant > 0.875)).clamp_min(MIN_EXP[dtype])
+    lo, hi = EXP[dtype]
+    e = torch.where(top == 0, lo, exp - 3 + (mant > 0.875)).clamp(lo, hi)
     y = torch.ldexp(torch.where(fine[..., None], x, 0).abs(), -e[..., None].float())
     u = torch.where(y < 2, (2 * y).round() / 2, torch.where(y < 4, y.round(), 2 * (y / 2).round()))
     return u.clamp_max(6).copysign(x), e, fine
@@ -358,7 +360,8 @@ def _stands_for(x, dtype):
     unit = torch.pow(2.0, torch.floor(torch.log2(top.clamp_min(1e-300))) - 2)
     unit = torch.where(top >= 8 * unit, unit * 2, unit)  # log2 of a value just below a power
     unit = torch.where(top < 4 * unit, unit / 2, unit)
-    unit = torch.where(top > 7 * unit, 2 * unit, unit).clamp_min(2.0 ** MIN_EXP[dtype])
+    lo, hi = EXP[dtype]
+    unit = torch.where(top > 7 * unit, 2 * unit, unit).clamp(2.0 ** lo, 2.0 ** hi)
     y = _e2m1(z.abs() / unit) * unit * torch.sign(z)
     return torch.where(torch.isfinite(top), y, math.nan).reshape(x.shape)
 
