@@ -25,6 +25,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = [
     "planner.cpp", "api.cpp", "merge.hip", "split_valu.hip", "split_mfma.hip", "planner_device.hip",
     "append.hip", "cost_model.cpp", "noalloc.hip", "noalloc_api.cpp",
+    "context/context_api.cpp", "context/attend.hip", "context/kv4_cache.hip", "context/prompt.hip",
 ]
 PROBE_SOURCES = ["read_probe.hip"]
 
@@ -39,7 +40,7 @@ EXTRA_FLAGS = {"merge.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=14"]}
 
 
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0].replace("/", "_") + ".o")
     cmd = [HIPCC, *COMMON_FLAGS]
     if src.endswith(".hip"):
         cmd += ["-x", "hip", *DEVICE_FLAGS, *EXTRA_FLAGS.get(src, [])]

@@ -1,0 +1,487 @@
+// Decode attention over the visible part of a paged cache (gfx950): one query
+// token per row, 16-bit pages or the 4-bit pool, d = 64 or 128, G <= 16.
+//
+//   out = sum_t exp(x_t - M) v_t / L,  x_t = scale <q, k_t>,  L = sum_t exp(x_t - M)
+// over the visible tokens t >= N - window or t < sinks.  One pass with the
+// running maximum and sum; a row's list of visible pages (the sinks' pages,
+// then the window's) is cut into splits whose partial states (m, l, o) a
+// second kernel joins.
+//
+// Bound: the bytes of the visible pages, read once.  A wave takes its pages in
+// units (16-bit: one page; 4-bit: two), the next unit's loads in flight while
+// one is computed.
+//  * Scores: v_mfma_f32_16x16x32, A = 16 tokens x 32 channels of K, B = Q^T (16
+//    heads, padded).  16-bit K arrives in coalesced rows and goes through a
+//    private, XOR-swizzled LDS tile into operand order; the 4-bit pool is
+//    stored in operand order and needs none.
+//  * P V: A = P (heads x tokens) from the lane's own scores, B = V (tokens x
+//    channels) by byte permutes.  P is split into its 16-bit rounding and the
+//    rounding of the rest, so the product keeps 16 (bf16) to 22 (f16) bits.
+//  * The maximum is only reduced over the wave when some score exceeds it.
+#include "context_internal.h"
+#include "kv4_common.h"
+#include "mfma.h"
+
+namespace pkv {
+namespace {
+
+// Pages of a split: the longest row's visible pages over the split cap.
+// Computed by every wave from the device lengths.
+__device__ __forceinline__ int split_pages(const AttendArgs& a) {
+  int t_max = 0;
+  for (int r = threadIdx.x & 63; r < a.batch; r += 64) {
+    const int n = clean_len(a.seq_lens[r], a.max_pages);
+    if (n > 0) t_max = max(t_max, seen_pages(n - 1, n - 1, a.window, a.sinks).count);
+  }
+  t_max = __builtin_amdgcn_readfirstlane(wave_max_i(t_max));
+  return max(1, (t_max + a.splits - 1) / a.splits);
+}
+
+// The loads of one page, as each format lays it out.
+template <int D, bool KV4>
+struct PageRegs;
+
+template <int D>
+struct PageRegs<D, true> {
+  uint32_t k[D / 32], v[D / 32];
+  uint32_t ks, vs;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane) {
+    const int kg = lane >> 4, c = lane & 15;
+    if constexpr (D == 128) {
+      const uint4 x = buffer_load16(r, lane * 16), y = buffer_load16(r, Kv4<D>::kV + lane * 16);
+      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+      v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+      ks = __builtin_amdgcn_raw_buffer_load_b32(r, Kv4<D>::kKs + c * 4, 0, kCachePolicyStream);
+    } else {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, 0, kCachePolicyStream);
+      const auto y = __builtin_amdgcn_raw_buffer_load_b64(r, Kv4<D>::kV + lane * 8, 0,
+                                                          kCachePolicyStream);
+      k[0] = x[0], k[1] = x[1];
+      v[0] = y[0], v[1] = y[1];
+      ks = __builtin_amdgcn_raw_buffer_load_b16(r, Kv4<D>::kKs + c * 2, 0, kCachePolicyStream);
+    }
+    // The lane's V channels lie in one block.
+    vs = __builtin_amdgcn_raw_buffer_load_b32(
+        r, Kv4<D>::kVs + kg * (D / 8) + (c / (512 / D)) * 4, 0, kCachePolicyStream);
+  }
+};
+
+template <int D>
+struct PageRegs<D, false> {
+  uint32_t k[4][D / 32], v[4][D / 32];  // tokens kg + 4 i, channels (D/16) c ..
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t kr, __amdgpu_buffer_rsrc_t vr,
+                                       int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (D == 128) {
+        const uint4 x = buffer_load16(kr, lane * 16 + i * 1024);
+        const uint4 y = buffer_load16(vr, lane * 16 + i * 1024);
+        k[i][0] = x.x, k[i][1] = x.y, k[i][2] = x.z, k[i][3] = x.w;
+        v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+      } else {
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(kr, lane * 8 + i * 512, 0,
+                                                            kCachePolicyStream);
+        const auto y = __builtin_amdgcn_raw_buffer_load_b64(vr, lane * 8 + i * 512, 0,
+                                                            kCachePolicyStream);
+        k[i][0] = x[0], k[i][1] = x[1];
+        v[i][0] = y[0], v[i][1] = y[1];
+      }
+    }
+  }
+};
+
+// The waves' states for the final combine; the K tiles share the space, which
+// they no longer need then.
+template <int D, int GP, int NW>
+struct AttendShared {
+  float m[NW][GP];
+  float l[NW][GP];
+  union {
+    alignas(16) float o[NW][GP][D];
+    uint4 k[NW][16][D / 8];  // per-wave K tile of 16-bit pages: [token][physical chunk]
+  };
+};
+
+// Physical 16-byte chunk of chunk ch of token t in a K tile: the 16 tokens that
+// the matrix core reads together lie on distinct banks, and so do the four
+// that a store writes.
+template <int D>
+__device__ __forceinline__ int ktile_chunk(int t, int ch) {
+  if constexpr (D == 128)
+    return ch ^ (((t & 3) << 2) | (t >> 2));
+  else
+    return ch ^ (((t & 3) << 1) | ((t >> 2) & 1));
+}
+
+template <int D, bool BF16, bool KV4, int GP, int NW, int PF>
+__global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
+  constexpr int UP = KV4 ? 2 : 1;  // pages per unit
+  constexpr int VEC = D / 16;      // channels per lane
+  constexpr int NT = D / 32;       // score products per page
+  __shared__ AttendShared<D, GP, NW> sh;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, kg = lane >> 4;
+  const int g = blockIdx.x, split = blockIdx.y, row = blockIdx.z;
+  const int G = a.group, hkv = a.num_kv_heads;
+  const int n = clean_len(a.seq_lens[row], a.max_pages);
+  if (n == 0) {  // an empty row sees nothing
+    if (split == 0) {
+      const int64_t h0 = int64_t(row) * a.num_q_heads + g * G;
+      for (int e = threadIdx.x; e < G * D; e += NW * 64)
+        static_cast<uint16_t*>(a.out)[h0 * D + e] = 0;
+      if (a.lse && threadIdx.x < G) a.lse[h0 + threadIdx.x] = kNegInf;
+    }
+    return;
+  }
+  const SeenPages sp = seen_pages(n - 1, n - 1, a.window, a.sinks);
+  const int pps = a.splits > 1 ? split_pages(a) : sp.count;
+  const int pb = split * pps;
+  const int pe = min(pb + pps, sp.count);
+  if (pb >= pe) return;
+  const bool whole = sp.count <= pps;  // the row has one split: no state to join
+  const int lo = (a.window > 0 && a.window < n) ? n - a.window : 0;
+
+  uint4 qb[NT];
+  {
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
+                         (int64_t(row) * a.num_q_heads + g * G + c) * D + 8 * kg;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) qb[t] = (c < G) ? load16(qp + 32 * t) : zero4();
+  }
+
+  float m_run = kLowest, l_part = 0.f;  // head c: running max (log2 units), this lane's sum
+  f32x4 acc[VEC];                       // O[4 kg + r][VEC c + j]
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // The wave's pages: units u = wave, wave + NW, ... of UP pages from pb.
+  const int32_t* bt = a.block_table + int64_t(row) * a.max_pages;
+  const int n_units = (pe - pb + UP - 1) / UP;
+  const int cnt = n_units > wave ? (n_units - wave + NW - 1) / NW : 0;
+  constexpr int CH = 64 / UP;  // units whose page ids one register holds
+  auto table_index = [&](int v) { return v < sp.ahead ? v : v + sp.skip; };
+  auto page_of = [&](int k) { return pb + UP * (wave + NW * k); };  // first page of unit k
+  auto load_ids = [&](int k0) {
+    const int v = page_of(k0 + lane / UP) + lane % UP;
+    const int id = (v < pe) ? bt[table_index(v)] : -1;
+    return (static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pool_pages)) ? id : -1;
+  };
+  int ids = load_ids(0), k0 = 0;
+
+  struct Unit {
+    PageRegs<D, KV4> page[UP];
+  };
+  auto issue = [&](int j, int n_c, Unit& u) {
+#pragma unroll
+    for (int x = 0; x < UP; ++x) {
+      const int id = (j < n_c) ? __builtin_amdgcn_readlane(ids, UP * j + x) : -1;
+      if constexpr (KV4) {
+        const uint8_t* p = static_cast<const uint8_t*>(a.k_pool) +
+                           (int64_t(max(id, 0)) * hkv + g) * Kv4<D>::kBytes;
+        u.page[x].load(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0,
+                                                         id >= 0 ? Kv4<D>::kBytes : 0,
+                                                         kBufferFlags),
+                       lane);
+      } else {
+        // Tokens past the row's length are not fetched: they read as zero.
+        const int base = table_index(page_of(k0 + j) + x) * 16;
+        const int bytes = id >= 0 ? min(16, n - base) * D * 2 : 0;
+        const int64_t at = (int64_t(max(id, 0)) * hkv + g) * 16 * D;
+        const uint16_t* kp = static_cast<const uint16_t*>(a.k_pool) + at;
+        const uint16_t* vp = static_cast<const uint16_t*>(a.v_pool) + at;
+        u.page[x].load(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(kp), (short)0,
+                                                         bytes, kBufferFlags),
+                       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(vp), (short)0,
+                                                         bytes, kBufferFlags),
+                       lane);
+      }
+    }
+  };
+
+  auto compute = [&](int j, Unit& u) {
+    float xs[4 * UP];
+#pragma unroll
+    for (int x = 0; x < UP; ++x) {
+      PageRegs<D, KV4>& pg = u.page[x];
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (KV4) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          s = mfma16<BF16>(kv4_eight<BF16>(pg.k[t], kv4_scale((pg.ks >> (8 * t)) & 0xff)), qb[t],
+                           s);
+      } else {
+        // K through the tile: the lane's tokens kg + 4 i, then A row m = c,
+        // token (c / 4) + 4 (c % 4), so that D row 4 kg + r is token kg + 4 r.
+        uint4 (&tile)[16][D / 8] = sh.k[wave];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = kg + 4 * i;
+          if constexpr (D == 128)
+            tile[t][ktile_chunk<D>(t, c)] = make_uint4(pg.k[i][0], pg.k[i][1], pg.k[i][2],
+                                                       pg.k[i][3]);
+          else
+            reinterpret_cast<uint2*>(&tile[t][ktile_chunk<D>(t, c >> 1)])[c & 1] =
+                make_uint2(pg.k[i][0], pg.k[i][1]);
+        }
+        const int at = (c >> 2) + 4 * (c & 3);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          s = mfma16<BF16>(tile[at][ktile_chunk<D>(at, 4 * t + kg)], qb[t], s);
+      }
+      const int v = page_of(k0 + j) + x;
+      const int base = table_index(v) * 16;
+      const int id = __builtin_amdgcn_readlane(ids, UP * j + x);
+      const bool full = id >= 0 && base + 16 <= n && (base >= lo || base + 16 <= a.sinks);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xs[4 * x + i] = s[i] * a.scale_log2;
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = base + (KV4 ? 4 * kg + i : kg + 4 * i);
+          const bool ok = id >= 0 && t < n && (t >= lo || t < a.sinks);
+          if (!ok) xs[4 * x + i] = kNegInf;
+          // An unseen token may hold anything: its V must be finite, as 0 * NaN
+          // is not 0.
+          if constexpr (KV4) {
+            if (!ok) pg.vs &= ~(0xffu << (8 * i));
+          } else {
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) pg.v[i][e] = ok ? pg.v[i][e] : 0u;
+          }
+        }
+      }
+    }
+    float top = xs[0];
+#pragma unroll
+    for (int i = 1; i < 4 * UP; ++i) top = fmaxf(top, xs[i]);
+    if (__builtin_amdgcn_ballot_w64(top > m_run) != 0) {  // rescale O and l to the new max
+      const float mn = fmaxf(m_run, max_x32(max_x16(top)));
+      const float alpha = fast_exp2(m_run - mn);
+      l_part *= alpha;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float ar = __int_as_float(
+            __builtin_amdgcn_ds_bpermute((4 * kg + r) << 2, __float_as_int(alpha)));
+#pragma unroll
+        for (int jj = 0; jj < VEC; ++jj) acc[jj][r] *= ar;
+      }
+      m_run = mn;
+    }
+    uint32_t ph[2 * UP], pl[2 * UP];
+#pragma unroll
+    for (int i = 0; i < 2 * UP; ++i) {
+      const float p0 = fast_exp2(xs[2 * i] - m_run), p1 = fast_exp2(xs[2 * i + 1] - m_run);
+      l_part += p0 + p1;
+      ph[i] = pack2<BF16>(p0, p1);
+      pl[i] = pack2<BF16>(p0 - Elem<BF16>::lo(ph[i]), p1 - Elem<BF16>::hi(ph[i]));
+    }
+    // V of the unit as [token][channel pair].
+    uint32_t w[4 * UP][VEC / 2];
+#pragma unroll
+    for (int x = 0; x < UP; ++x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (KV4) {
+          const float sc = kv4_scale((u.page[x].vs >> (8 * i)) & 0xff);
+          if constexpr (D == 128) {
+            const uint4 e = kv4_eight<BF16>(u.page[x].v[i], sc);
+            w[4 * x + i][0] = e.x, w[4 * x + i][1] = e.y;
+            w[4 * x + i][2] = e.z, w[4 * x + i][3] = e.w;
+          } else {
+            const uint32_t two = u.page[x].v[i >> 1];  // tokens 2 (i / 2) and the next
+            w[4 * x + i][0] = (i & 1) ? kv4_pair<BF16, 2>(two, sc) : kv4_pair<BF16, 0>(two, sc);
+            w[4 * x + i][1] = (i & 1) ? kv4_pair<BF16, 3>(two, sc) : kv4_pair<BF16, 1>(two, sc);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC / 2; ++e) w[4 * x + i][e] = u.page[x].v[i][e];
+        }
+      }
+    }
+#pragma unroll
+    for (int jj = 0; jj < VEC; ++jj) {
+      const uint32_t sel = (jj & 1) ? 0x07060302u : 0x05040100u;
+      uint32_t b[2 * UP];
+#pragma unroll
+      for (int i = 0; i < 2 * UP; ++i)
+        b[i] = __builtin_amdgcn_perm(w[2 * i + 1][jj >> 1], w[2 * i][jj >> 1], sel);
+      if constexpr (UP == 2) {
+        const uint4 bv = make_uint4(b[0], b[1], b[2], b[3]);
+        acc[jj] = mfma16<BF16>(make_uint4(ph[0], ph[1], ph[2], ph[3]), bv, acc[jj]);
+        acc[jj] = mfma16<BF16>(make_uint4(pl[0], pl[1], pl[2], pl[3]), bv, acc[jj]);
+      } else {
+        const uint2 bv = make_uint2(b[0], b[1]);
+        acc[jj] = mfma16_k16<BF16>(make_uint2(ph[0], ph[1]), bv, acc[jj]);
+        acc[jj] = mfma16_k16<BF16>(make_uint2(pl[0], pl[1]), bv, acc[jj]);
+      }
+    }
+  };
+
+  constexpr int R = PF + 1;
+  Unit ring[R];
+  for (k0 = 0; k0 < cnt; k0 += CH) {
+    const int n_c = min(CH, cnt - k0);
+    if (k0 > 0) ids = load_ids(k0);
+#pragma unroll
+    for (int u = 0; u < PF; ++u) issue(u, n_c, ring[u]);
+    for (int j0 = 0; j0 < n_c; j0 += R) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        issue(j0 + u + PF, n_c, ring[(u + PF) % R]);
+        if (j0 + u < n_c) compute(j0 + u, ring[u]);
+      }
+    }
+  }
+
+  // ---- combine the waves ------------------------------------------------------
+  const float l_tot = sum_x32(sum_x16(l_part));
+  __syncthreads();  // every wave is done with its K tile
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int h = 4 * kg + r;
+    if (h < GP) {
+#pragma unroll
+      for (int jj = 0; jj < VEC; ++jj) sh.o[wave][h][VEC * c + jj] = acc[jj][r];
+    }
+  }
+  if (lane < GP) {
+    sh.m[wave][lane] = m_run;
+    sh.l[wave][lane] = l_tot;
+  }
+  __syncthreads();
+  constexpr int C4 = D / 4;
+  const int64_t pair = int64_t(row) * hkv + g;
+  const int64_t slot = pair * a.splits + split;
+  for (int e = threadIdx.x; e < G * C4; e += NW * 64) {
+    const int h = e / C4, c4 = e % C4;
+    float mx = kLowest;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sh.m[w][h]);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float wt = fast_exp2(sh.m[w][h] - mx);
+      const float4 ow = reinterpret_cast<const float4*>(sh.o[w][h])[c4];
+      l = fmaf(wt, sh.l[w][h], l);
+      o.x = fmaf(wt, ow.x, o.x);
+      o.y = fmaf(wt, ow.y, o.y);
+      o.z = fmaf(wt, ow.z, o.z);
+      o.w = fmaf(wt, ow.w, o.w);
+    }
+    if (whole) {
+      const int64_t qh = int64_t(row) * a.num_q_heads + g * G + h;
+      const bool none = l == 0.f;  // every page of the row lies outside the pool
+      const float inv = none ? 0.f : 1.f / l;
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[c4] =
+          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+      if (c4 == 0 && a.lse) a.lse[qh] = none ? kNegInf : mx * kLn2 + __logf(l);
+    } else {
+      reinterpret_cast<float4*>(a.st_o + (slot * G + h) * D)[c4] = o;
+      if (c4 == 0) {
+        a.st_m[slot * G + h] = mx;
+        a.st_l[slot * G + h] = l;
+      }
+    }
+  }
+}
+
+// Joins the splits of one (row, query head): M = max m_s, w_s = 2^(m_s - M),
+// out = sum w_s o_s / sum w_s l_s.  256 threads: D/4 chunks of four floats
+// times as many split groups.
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
+  constexpr int CH = D / 4, SG = 256 / CH;
+  const int h = blockIdx.x, row = blockIdx.y;
+  const int n = clean_len(a.seq_lens[row], a.max_pages);
+  if (n == 0) return;
+  const SeenPages sp = seen_pages(n - 1, n - 1, a.window, a.sinks);
+  const int pps = split_pages(a);
+  const int ns = (sp.count + pps - 1) / pps;
+  if (ns == 1) return;  // written by its only split
+  const int g = h / a.group, hh = h % a.group;
+  const int64_t base = (int64_t(row) * a.num_kv_heads + g) * a.splits;
+  const int ch = threadIdx.x % CH, sg = threadIdx.x / CH;
+  float m = kLowest, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = sg; s < ns; s += SG) {
+    const int64_t e = (base + s) * a.group + hh;
+    const float ms = a.st_m[e], ls = a.st_l[e];
+    const float4 os = reinterpret_cast<const float4*>(a.st_o + e * D)[ch];
+    const float mn = fmaxf(m, ms);
+    const float a1 = fast_exp2(m - mn), a2 = fast_exp2(ms - mn);
+    l = l * a1 + ls * a2;
+    o.x = o.x * a1 + os.x * a2;
+    o.y = o.y * a1 + os.y * a2;
+    o.z = o.z * a1 + os.z * a2;
+    o.w = o.w * a1 + os.w * a2;
+    m = mn;
+  }
+  __shared__ float s_m[SG], s_l[SG];
+  __shared__ float4 s_o[SG][CH];
+  if (ch == 0) {
+    s_m[sg] = m;
+    s_l[sg] = l;
+  }
+  s_o[sg][ch] = o;
+  __syncthreads();
+  if (threadIdx.x >= CH) return;
+  m = kLowest;
+#pragma unroll
+  for (int k = 0; k < SG; ++k) m = fmaxf(m, s_m[k]);
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < SG; ++k) {
+    const float w = fast_exp2(s_m[k] - m);
+    const float4 v = s_o[k][ch];
+    l = fmaf(w, s_l[k], l);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const int64_t qh = int64_t(row) * a.num_q_heads + h;
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[ch] =
+      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+  if (ch == 0 && a.lse) a.lse[qh] = none ? kNegInf : m * kLn2 + __logf(l);
+}
+
+template <int D, bool BF16, bool KV4>
+void launch_gp(const AttendArgs& a, hipStream_t s) {
+  const dim3 grid(a.num_kv_heads, a.splits, a.batch);
+  constexpr int PF = KV4 ? 2 : 1;
+  if (a.group <= 4)
+    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 4, 4, PF>), grid, dim3(256), 0, s, a);
+  else if (a.group <= 8)
+    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 8, 4, PF>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 16, 4, PF>), grid, dim3(256), 0, s, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((join_kernel<D, BF16>), dim3(a.num_q_heads, a.batch), dim3(256), 0, s, a);
+}
+
+template <int D, bool BF16>
+void launch_fmt(bool kv4, const AttendArgs& a, hipStream_t s) {
+  if (kv4) launch_gp<D, BF16, true>(a, s);
+  else launch_gp<D, BF16, false>(a, s);
+}
+
+}  // namespace
+
+pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& a, hipStream_t s) {
+  const bool bf = p.dtype == PKV_BF16;
+  if (p.head_dim == 128) {
+    if (bf) launch_fmt<128, true>(kv4, a, s);
+    else launch_fmt<128, false>(kv4, a, s);
+  } else {
+    if (bf) launch_fmt<64, true>(kv4, a, s);
+    else launch_fmt<64, false>(kv4, a, s);
+  }
+  return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
+}
+
+}  // namespace pkv

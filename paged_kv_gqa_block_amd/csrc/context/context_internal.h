@@ -1,0 +1,145 @@
+// Internal declarations of the context operators (include/pkv_context.h):
+// kernel arguments, launchers and the view arithmetic that host and device
+// share.  Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include "pkv_context.h"
+
+#if defined(__HIP__) || defined(__HIPCC__)
+#define PKV_HD __host__ __device__ __forceinline__
+#else
+#define PKV_HD inline
+#endif
+
+namespace pkv {
+
+// The pages of one row that some query of a run sees, in reading order: the
+// sinks' pages, then the window's.  Page v of that list is block-table entry
+// v < ahead ? v : v + skip.
+struct SeenPages {
+  int ahead;  // pages that hold sinks only
+  int skip;   // pages between them and the window
+  int count;
+};
+
+// Queries at positions first_q .. last_q (0 <= first_q <= last_q).
+PKV_HD SeenPages seen_pages(int first_q, int last_q, int window, int sinks) {
+  const int begin = (window > 0 && first_q >= window) ? (first_q - window + 1) >> 4 : 0;
+  const int sink_pages = (sinks >> 4) + ((sinks & 15) ? 1 : 0);
+  SeenPages s;
+  s.ahead = sink_pages < begin ? sink_pages : begin;
+  s.skip = begin - s.ahead;
+  s.count = (last_q >> 4) + 1 - s.skip;
+  return s;
+}
+
+// Whether the query at position p sees token t.
+PKV_HD bool sees(int p, int t, int window, int sinks) {
+  return t <= p && (window == 0 || t > p - window || t < sinks);
+}
+
+struct AttendArgs {
+  const void* q;        // [B][Hq][d]
+  const void* k_pool;   // 16-bit pages, or the 4-bit pool (v_pool unused)
+  const void* v_pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  float* st_m;          // [slots][G], log2 units
+  float* st_l;
+  float* st_o;          // [slots][G][d]
+  int32_t* arrivals;    // [B * Hkv], zero between calls
+  void* out;
+  float* lse;           // may be null
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t max_pages;
+  int32_t num_pool_pages;
+  int32_t splits;
+  int32_t window;       // 0: everything
+  int32_t sinks;
+  float scale_log2;
+};
+
+struct PromptArgs {
+  const void* q;        // [num_tokens][Hq][d]
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tok_offsets;  // [B + 1]
+  void* out;
+  float* lse;
+  int32_t batch;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t max_pages;
+  int32_t num_pool_pages;
+  int32_t window;
+  int32_t sinks;
+  float scale_log2;
+};
+
+struct StoreArgs {
+  const void* k_new;    // token stride k_stride elements, heads contiguous
+  const void* v_new;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tok_offsets;  // null: one token per row
+  void* k_pool;         // 16-bit pages, or the 4-bit pool (v_pool unused)
+  void* v_pool;
+  int32_t batch;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t max_pages;
+  int32_t num_pool_pages;
+};
+
+struct LoadArgs {
+  const void* pool;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* tok_offsets;
+  void* k_out;          // [num_tokens][Hkv][d]
+  void* v_out;
+  int32_t batch;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t max_pages;
+  int32_t num_pool_pages;
+};
+
+// Page segments of a run: a bound that needs only the token count.  Row i owns
+// the segments [off_i / 16 + 2 i, off_{i+1} / 16 + 2 (i + 1)), at least the
+// ceil(n_i / 16) + 1 pages its run can touch.
+PKV_HD int64_t segment_base(int64_t off, int64_t row) { return (off >> 4) + 2 * row; }
+
+// Workgroups of a store or load launch: every segment of every KV head.
+template <typename Args>
+inline int64_t run_groups(const Args& a) {
+  return (a.tok_offsets ? segment_base(a.num_tokens, a.batch) : a.batch) * a.num_kv_heads;
+}
+
+// Query tiles of a prompt, by the same rule over packed rows (token, head of
+// the group).
+constexpr int kTileRows = 128;
+PKV_HD int64_t tile_base(int64_t off, int64_t row, int group) {
+  return off * group / kTileRows + row;
+}
+inline int64_t prompt_tiles(const PromptArgs& a) {
+  return a.tok_offsets ? tile_base(a.num_tokens, a.batch, a.group) : int64_t(a.batch);
+}
+
+pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& a, hipStream_t s);
+pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hipStream_t s);
+pkv_status launch_store(const pkv_problem& p, bool kv4, const StoreArgs& a, hipStream_t s);
+pkv_status launch_load(const pkv_problem& p, const LoadArgs& a, hipStream_t s);
+
+}  // namespace pkv

@@ -13,7 +13,7 @@ import os
 import numpy as np
 import torch
 
-from . import _lib
+from . import _context, _lib
 from ._lib import (PATH_IDS, PATH_NAMES, PKV_NOSPLIT, PKV_WORKQUEUE, make_problem, pkv_decode,
                    pkv_decode_device, pkv_merge, pkv_merge_device, pkv_plan, pkv_plan_bytes,
                    pkv_plan_device, pkv_policy)
@@ -173,6 +173,213 @@ class SelfPlannedStep(_PersistentStepBuffers):
                                  self.st_l, self.st_o, stream=stream)
         _lib.pkv_merge_selfplan(self.prob, w["seq_lens"], self.splits, self.counter, self.st_m,
                                 self.st_l, self.st_o, self.out, self.lse, stream=stream)
+        return self.out, self.lse
+
+
+class _ContextCalls:
+    """Argument checks and stream choice shared by the context operators
+    (include/pkv_context.h).  They run on the device of their buffers, on the
+    given stream or that device's current one."""
+
+    def __init__(self, prob: _lib.pkv_problem, device):
+        self.prob = prob
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.dtype = torch.bfloat16 if prob.dtype == _lib.PKV_BF16 else torch.float16
+        self.kv4_page_bytes = _context.pkv_kv4_page_bytes(prob.head_dim)
+
+    def _stream(self, stream):
+        return stream if stream is not None else torch.cuda.current_stream(self.device)
+
+    def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> torch.Tensor:
+        if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} "
+                             f"{dtype} on {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    def _tables(self, block_table, seq_lens) -> None:
+        p = self.prob
+        self._expect("block_table", block_table, (p.batch, p.max_pages_per_row), torch.int32)
+        self._expect("seq_lens", seq_lens, (p.batch,), torch.int32)
+
+    def _offsets(self, tok_offsets, num_tokens: int) -> None:
+        if tok_offsets is not None:
+            self._expect("tok_offsets", tok_offsets, (self.prob.batch + 1,), torch.int32)
+        elif num_tokens != self.prob.batch:
+            raise ValueError(f"{num_tokens} tokens of {self.prob.batch} rows need tok_offsets")
+
+    def _kv4_pool(self, pool) -> None:
+        p = self.prob
+        self._expect("kv4_pool", pool, (p.num_pool_pages, p.num_kv_heads, self.kv4_page_bytes),
+                     torch.uint8)
+
+    def _pools(self, w: dict) -> tuple:
+        """The cache of `w`: (True, its 4-bit pool) or (False, its two 16-bit pools)."""
+        p = self.prob
+        if "kv4_pool" in w:
+            self._kv4_pool(w["kv4_pool"])
+            return True, w["kv4_pool"]
+        shape = (p.num_pool_pages, p.num_kv_heads, p.page_size, p.head_dim)
+        self._expect("k_pool", w["k_pool"], shape, self.dtype)
+        self._expect("v_pool", w["v_pool"], shape, self.dtype)
+        return False, (w["k_pool"], w["v_pool"])
+
+
+class Kv4Cache(_ContextCalls):
+    """The paged cache held in 4 bits: K and V of one layer in one byte pool.
+
+    ``store`` quantises a run of new tokens as it writes them and ``load``
+    reads a run back; ``Kv4Step`` and ``PromptStep`` attend over ``pool``.
+    """
+
+    def __init__(self, prob: _lib.pkv_problem, pool: torch.Tensor | None = None, device="cuda"):
+        super().__init__(prob, pool.device if pool is not None else device)
+        if pool is None:
+            pool = torch.zeros(prob.num_pool_pages, prob.num_kv_heads, self.kv4_page_bytes,
+                               dtype=torch.uint8, device=self.device)
+        self._kv4_pool(pool)
+        self.pool = pool
+
+    def store(self, k_new, v_new, block_table, seq_lens, tok_offsets=None, stream=None) -> None:
+        """k_new, v_new: [tokens][Hkv][d], heads contiguous, any token stride
+        that is a multiple of 8; seq_lens: the lengths after them; tok_offsets:
+        [B + 1], or None for one token per row."""
+        p, n = self.prob, k_new.shape[0]
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            if (tuple(t.shape) != (n, p.num_kv_heads, p.head_dim) or t.dtype != self.dtype
+                    or t.device != self.device):
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
+        self._tables(block_table, seq_lens)
+        self._offsets(tok_offsets, n)
+        with torch.cuda.device(self.device):
+            _context.pkv_kv4_store(p, tok_offsets, n, seq_lens, k_new, v_new, block_table,
+                                   self.pool, self._stream(stream))
+
+    def load(self, block_table, seq_lens, tok_offsets, k_out, v_out, stream=None) -> tuple:
+        """The values the cache stands for, into k_out, v_out [tokens][Hkv][d]."""
+        p, n = self.prob, k_out.shape[0]
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            self._expect(name, t, (n, p.num_kv_heads, p.head_dim), self.dtype)
+        self._tables(block_table, seq_lens)
+        self._offsets(tok_offsets, n)
+        with torch.cuda.device(self.device):
+            _context.pkv_kv4_load(p, tok_offsets, n, seq_lens, block_table, self.pool, k_out,
+                                  v_out, self._stream(stream))
+        return k_out, v_out
+
+
+def store_kv(prob: _lib.pkv_problem, k_new, v_new, block_table, seq_lens, tok_offsets, k_pool,
+             v_pool, stream=None) -> None:
+    """Write a run of new tokens into the 16-bit pools (arguments as
+    ``Kv4Cache.store``)."""
+    calls, n = _ContextCalls(prob, k_pool.device), k_new.shape[0]
+    calls._pools({"k_pool": k_pool, "v_pool": v_pool})
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if (tuple(t.shape) != (n, prob.num_kv_heads, prob.head_dim) or t.dtype != calls.dtype
+                or t.device != calls.device):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
+    calls._tables(block_table, seq_lens)
+    calls._offsets(tok_offsets, n)
+    with torch.cuda.device(calls.device):
+        _context.pkv_store_kv(prob, tok_offsets, n, seq_lens, k_new, v_new, block_table, k_pool,
+                              v_pool, calls._stream(stream))
+
+
+class WindowStep(_ContextCalls):
+    """One decode step over the visible part of a 16-bit cache: the last
+    `window` tokens (0: all) and the first `sinks`.
+
+    Owns the output and the workspace, so calls of one step must not overlap.
+    ``run`` takes the dict of ``DecodeStep.run`` (q, k_pool, v_pool,
+    block_table, seq_lens); ``bind`` / ``run_bound`` are its form with the
+    arguments checked and marshalled once, for loops over fixed buffers.
+    """
+
+    _call = "pkv_attend_window"
+
+    def __init__(self, prob: _lib.pkv_problem, window: int = 0, sinks: int = 0,
+                 splits: int | None = None, device="cuda"):
+        super().__init__(prob, device)
+        self.view = _context.make_view(window, sinks)
+        if splits is None:
+            splits = _context.pkv_attend_splits(
+                prob, self.view, torch.cuda.get_device_properties(
+                    self.device).multi_processor_count)
+        self.splits = splits
+        nbytes = _context.pkv_attend_workspace_bytes(prob, splits)
+        if nbytes == 0:
+            raise _lib.PkvError("pkv_attend_workspace_bytes", _lib.PKV_EINVAL, "invalid problem")
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.out = torch.empty(prob.batch, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
+                               device=self.device)
+        self.lse = torch.empty(prob.batch, prob.num_q_heads, dtype=torch.float32,
+                               device=self.device)
+
+    def bind(self, w: dict, stream=None) -> tuple:
+        p = self.prob
+        self._expect("q", w["q"], (p.batch, p.num_q_heads, p.head_dim), self.dtype)
+        self._tables(w["block_table"], w["seq_lens"])
+        kv4, pools = self._pools(w)
+        if kv4 != (self._call == "pkv_attend_kv4"):
+            raise ValueError(f"{type(self).__name__} over the wrong kind of cache")
+        return _lib.bind_call(self._call, p, self.view, w["seq_lens"], self.splits, w["q"],
+                              *((pools,) if kv4 else pools), w["block_table"], self.workspace,
+                              self.workspace.numel(), self.out, self.lse, self._stream(stream))
+
+    def run(self, w: dict, stream=None) -> tuple:
+        return self.run_bound(self.bind(w, stream))
+
+    def run_bound(self, bound: tuple) -> tuple:
+        with torch.cuda.device(self.device):
+            _lib.call_bound(bound)
+        return self.out, self.lse
+
+
+class Kv4Step(WindowStep):
+    """One decode step over the 4-bit cache (q, kv4_pool, block_table,
+    seq_lens), with the view of ``WindowStep``."""
+
+    _call = "pkv_attend_kv4"
+
+
+class PromptStep(_ContextCalls):
+    """Causal attention of up to `num_tokens` new tokens, all rows together,
+    over a 16-bit or 4-bit cache that already holds them.
+
+    ``run`` takes q [num_tokens][Hq][d], tok_offsets [B + 1] (or None for one
+    token per row), block_table, seq_lens and k_pool, v_pool or kv4_pool.
+    """
+
+    def __init__(self, prob: _lib.pkv_problem, num_tokens: int, window: int = 0, sinks: int = 0,
+                 device="cuda"):
+        super().__init__(prob, device)
+        self.view = _context.make_view(window, sinks)
+        self.num_tokens = num_tokens
+        self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
+                               device=self.device)
+        self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
+                               device=self.device)
+
+    def bind(self, w: dict, stream=None) -> tuple:
+        p, off = self.prob, w.get("tok_offsets")
+        self._expect("q", w["q"], (self.num_tokens, p.num_q_heads, p.head_dim), self.dtype)
+        self._tables(w["block_table"], w["seq_lens"])
+        self._offsets(off, self.num_tokens)
+        kv4, pools = self._pools(w)
+        return _lib.bind_call("pkv_prompt_kv4" if kv4 else "pkv_prompt_window", p, self.view, off,
+                              self.num_tokens, w["seq_lens"], w["q"],
+                              *((pools,) if kv4 else pools), w["block_table"], self.out, self.lse,
+                              self._stream(stream))
+
+    def run(self, w: dict, stream=None) -> tuple:
+        return self.run_bound(self.bind(w, stream))
+
+    def run_bound(self, bound: tuple) -> tuple:
+        with torch.cuda.device(self.device):
+            _lib.call_bound(bound)
         return self.out, self.lse
 
 
