@@ -52,7 +52,7 @@ def pkv_kv4_page_bytes(head_dim: int) -> int:
     return LIB.pkv_kv4_page_bytes(head_dim)
 
 
-def _token_stride(x) -> int:
+def token_stride(x) -> int:
     """Elements between the tokens of [tokens][Hkv][d] with contiguous heads."""
     if x.dim() != 3 or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
         raise ValueError("new keys and values are [tokens][Hkv][d] with contiguous heads")
@@ -64,7 +64,7 @@ def pkv_store_kv(prob, tok_offsets, num_tokens: int, seq_lens_dev, k_new, v_new,
                  k_pool, v_pool, stream=None) -> None:
     _check("pkv_store_kv", LIB.pkv_store_kv(
         ctypes.byref(prob), _ptr(tok_offsets), num_tokens, _ptr(seq_lens_dev), k_new.data_ptr(),
-        _token_stride(k_new), v_new.data_ptr(), _token_stride(v_new), _ptr(block_table),
+        token_stride(k_new), v_new.data_ptr(), token_stride(v_new), _ptr(block_table),
         _ptr(k_pool), _ptr(v_pool), _stream(stream)))
 
 
@@ -72,7 +72,7 @@ def pkv_kv4_store(prob, tok_offsets, num_tokens: int, seq_lens_dev, k_new, v_new
                   kv4_pool, stream=None) -> None:
     _check("pkv_kv4_store", LIB.pkv_kv4_store(
         ctypes.byref(prob), _ptr(tok_offsets), num_tokens, _ptr(seq_lens_dev), k_new.data_ptr(),
-        _token_stride(k_new), v_new.data_ptr(), _token_stride(v_new), _ptr(block_table),
+        token_stride(k_new), v_new.data_ptr(), token_stride(v_new), _ptr(block_table),
         _ptr(kv4_pool), _stream(stream)))
 
 

@@ -4,8 +4,8 @@
 //   out = sum_t exp(x_t - M) v_t / L,  x_t = scale <q, k_t>,  L = sum_t exp(x_t - M)
 // over the visible tokens t >= N - window or t < sinks.  One pass with the
 // running maximum and sum; a row's list of visible pages (the sinks' pages,
-// then the window's) is cut into splits whose partial states (m, l, o) a
-// second kernel joins.
+// then the window's) is cut into splits; each leaves its partial state (m, l,
+// o), and the last of them to finish joins the pair's states: one launch.
 //
 // Bound: the bytes of the visible pages, read once.  A wave takes its pages in
 // units (16-bit: one page; 4-bit: two), the next unit's loads in flight while
@@ -17,7 +17,11 @@
 //  * P V: A = P (heads x tokens) from the lane's own scores, B = V (tokens x
 //    channels) by byte permutes.  P is split into its 16-bit rounding and the
 //    rounding of the rest, so the product keeps 16 (bf16) to 22 (f16) bits.
-//  * The maximum is only reduced over the wave when some score exceeds it.
+//  * The running maximum only moves, and O is only rescaled, when a score passes
+//    it by more than 2^8 (kSlack): below that the weights stay exact enough in
+//    fp32 and fit in f16.
+// Three waves of a SIMD (at most 168 registers): with the compiler's own two,
+// 96 rows x 8 heads x 8192 tokens in 4 bits took 190 us instead of 160.
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
@@ -113,12 +117,68 @@ __device__ __forceinline__ int ktile_chunk(int t, int ch) {
     return ch ^ (((t & 3) << 1) | ((t >> 2) & 1));
 }
 
+// Partial states cross from one XCD's L2 to another's inside a launch: stores
+// and loads at agent scope pass through both.
+__device__ __forceinline__ void put_state(float* p, float x, float y) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p),
+                     __builtin_bit_cast(uint64_t, make_float2(x, y)), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put_state(float* p, const float4& o) {
+  put_state(p, o.x, o.y);
+  put_state(p + 2, o.z, o.w);
+}
+__device__ __forceinline__ float2 get_state2(const float* p) {
+  return __builtin_bit_cast(
+      float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ float4 get_state4(const float* p) {
+  const float2 a = get_state2(p), b = get_state2(p + 2);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// (m, l, o) joined with (m1, l1, o1).
+__device__ __forceinline__ void join(float& m, float& l, float4& o, float m1, float l1,
+                                     const float4& o1) {
+  const float mn = fmaxf(m, m1);
+  const float w0 = fast_exp2(m - mn), w1 = fast_exp2(m1 - mn);
+  l = l * w0 + l1 * w1;
+  o.x = o.x * w0 + o1.x * w1;
+  o.y = o.y * w0 + o1.y * w1;
+  o.z = o.z * w0 + o1.z * w1;
+  o.w = o.w * w0 + o1.w * w1;
+  m = mn;
+}
+
+// Four channels of a query head's output, and its lse.
+template <int D, bool BF16>
+__device__ __forceinline__ void write_out(const AttendArgs& a, int64_t qh, int c4, float m, float l,
+                                          const float4& o) {
+  const bool none = l == 0.f;  // every page of the row lies outside the pool
+  const float inv = none ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[c4] =
+      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+  if (c4 == 0 && a.lse) a.lse[qh] = none ? kNegInf : m * kLn2 + __logf(l);
+}
+
+// P V for one lane column of channels: 16 tokens, or 32.
+template <bool BF16>
+__device__ __forceinline__ f32x4 pv(const uint32_t (&p)[2], const uint32_t (&v)[2], f32x4 c) {
+  return mfma16_k16<BF16>(make_uint2(p[0], p[1]), make_uint2(v[0], v[1]), c);
+}
+template <bool BF16>
+__device__ __forceinline__ f32x4 pv(const uint32_t (&p)[4], const uint32_t (&v)[4], f32x4 c) {
+  return mfma16<BF16>(make_uint4(p[0], p[1], p[2], p[3]), make_uint4(v[0], v[1], v[2], v[3]), c);
+}
+
 template <int D, bool BF16, bool KV4, int GP, int NW, int PF>
-__global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3,8))) void attend_kernel(AttendArgs a) {
   constexpr int UP = KV4 ? 2 : 1;  // pages per unit
   constexpr int VEC = D / 16;      // channels per lane
   constexpr int NT = D / 32;       // score products per page
   __shared__ AttendShared<D, GP, NW> sh;
+  __shared__ bool s_last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, kg = lane >> 4;
@@ -147,7 +207,10 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
     const uint16_t* qp = static_cast<const uint16_t*>(a.q) +
                          (int64_t(row) * a.num_q_heads + g * G + c) * D + 8 * kg;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) qb[t] = (c < G) ? load16(qp + 32 * t) : zero4();
+    for (int t = 0; t < NT; ++t) {
+      qb[t] = (c < G) ? load16(qp + 32 * t) : zero4();
+      qb[t].x ^= a.q_flip, qb[t].y ^= a.q_flip, qb[t].z ^= a.q_flip, qb[t].w ^= a.q_flip;
+    }
   }
 
   float m_run = kLowest, l_part = 0.f;  // head c: running max (log2 units), this lane's sum
@@ -234,7 +297,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
       const int id = __builtin_amdgcn_readlane(ids, UP * j + x);
       const bool full = id >= 0 && base + 16 <= n && (base >= lo || base + 16 <= a.sinks);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[4 * x + i] = s[i] * a.scale_log2;
+      for (int i = 0; i < 4; ++i) xs[4 * x + i] = s[i];
       if (!full) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -255,7 +318,8 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
     float top = xs[0];
 #pragma unroll
     for (int i = 1; i < 4 * UP; ++i) top = fmaxf(top, xs[i]);
-    if (__builtin_amdgcn_ballot_w64(top > m_run) != 0) {  // rescale O and l to the new max
+    top *= a.scale_log2;
+    if (__builtin_amdgcn_ballot_w64(top > m_run + kSlack) != 0) {  // rescale O and l
       const float mn = fmaxf(m_run, max_x32(max_x16(top)));
       const float alpha = fast_exp2(m_run - mn);
       l_part *= alpha;
@@ -271,7 +335,8 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
     uint32_t ph[2 * UP], pl[2 * UP];
 #pragma unroll
     for (int i = 0; i < 2 * UP; ++i) {
-      const float p0 = fast_exp2(xs[2 * i] - m_run), p1 = fast_exp2(xs[2 * i + 1] - m_run);
+      const float p0 = fast_exp2(fmaf(xs[2 * i], a.scale_log2, -m_run));
+      const float p1 = fast_exp2(fmaf(xs[2 * i + 1], a.scale_log2, -m_run));
       l_part += p0 + p1;
       ph[i] = pack2<BF16>(p0, p1);
       pl[i] = pack2<BF16>(p0 - Elem<BF16>::lo(ph[i]), p1 - Elem<BF16>::hi(ph[i]));
@@ -299,23 +364,17 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
         }
       }
     }
+    uint32_t b[VEC][2 * UP];
 #pragma unroll
     for (int jj = 0; jj < VEC; ++jj) {
       const uint32_t sel = (jj & 1) ? 0x07060302u : 0x05040100u;
-      uint32_t b[2 * UP];
 #pragma unroll
       for (int i = 0; i < 2 * UP; ++i)
-        b[i] = __builtin_amdgcn_perm(w[2 * i + 1][jj >> 1], w[2 * i][jj >> 1], sel);
-      if constexpr (UP == 2) {
-        const uint4 bv = make_uint4(b[0], b[1], b[2], b[3]);
-        acc[jj] = mfma16<BF16>(make_uint4(ph[0], ph[1], ph[2], ph[3]), bv, acc[jj]);
-        acc[jj] = mfma16<BF16>(make_uint4(pl[0], pl[1], pl[2], pl[3]), bv, acc[jj]);
-      } else {
-        const uint2 bv = make_uint2(b[0], b[1]);
-        acc[jj] = mfma16_k16<BF16>(make_uint2(ph[0], ph[1]), bv, acc[jj]);
-        acc[jj] = mfma16_k16<BF16>(make_uint2(pl[0], pl[1]), bv, acc[jj]);
-      }
+        b[jj][i] = __builtin_amdgcn_perm(w[2 * i + 1][jj >> 1], w[2 * i][jj >> 1], sel);
+      acc[jj] = pv<BF16>(ph, b[jj], acc[jj]);
     }
+#pragma unroll
+    for (int jj = 0; jj < VEC; ++jj) acc[jj] = pv<BF16>(pl, b[jj], acc[jj]);
   };
 
   constexpr int R = PF + 1;
@@ -371,83 +430,76 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a) {
       o.w = fmaf(wt, ow.w, o.w);
     }
     if (whole) {
-      const int64_t qh = int64_t(row) * a.num_q_heads + g * G + h;
-      const bool none = l == 0.f;  // every page of the row lies outside the pool
-      const float inv = none ? 0.f : 1.f / l;
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[c4] =
-          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
-      if (c4 == 0 && a.lse) a.lse[qh] = none ? kNegInf : mx * kLn2 + __logf(l);
+      write_out<D, BF16>(a, int64_t(row) * a.num_q_heads + g * G + h, c4, mx, l, o);
     } else {
-      reinterpret_cast<float4*>(a.st_o + (slot * G + h) * D)[c4] = o;
-      if (c4 == 0) {
-        a.st_m[slot * G + h] = mx;
-        a.st_l[slot * G + h] = l;
-      }
+      put_state(a.st_o + (slot * G + h) * D + 4 * c4, o);
+      if (c4 == 0) put_state(a.st_ml + (slot * G + h) * 2, mx, l);
     }
   }
-}
+  if (whole) return;
 
-// Joins the splits of one (row, query head): M = max m_s, w_s = 2^(m_s - M),
-// out = sum w_s o_s / sum w_s l_s.  256 threads: D/4 chunks of four floats
-// times as many split groups.
-template <int D, bool BF16>
-__global__ __launch_bounds__(256) void join_kernel(AttendArgs a) {
-  constexpr int CH = D / 4, SG = 256 / CH;
-  const int h = blockIdx.x, row = blockIdx.y;
-  const int n = clean_len(a.seq_lens[row], a.max_pages);
-  if (n == 0) return;
-  const SeenPages sp = seen_pages(n - 1, n - 1, a.window, a.sinks);
-  const int pps = split_pages(a);
+  // ---- the last split of the pair to arrive joins them all -------------------------
+  // Its sum runs in split order, so the result does not depend on who arrives
+  // last.  M = max m_s, w_s = 2^(m_s - M), out = sum w_s o_s / sum w_s l_s.
   const int ns = (sp.count + pps - 1) / pps;
-  if (ns == 1) return;  // written by its only split
-  const int g = h / a.group, hh = h % a.group;
-  const int64_t base = (int64_t(row) * a.num_kv_heads + g) * a.splits;
-  const int ch = threadIdx.x % CH, sg = threadIdx.x / CH;
-  float m = kLowest, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = sg; s < ns; s += SG) {
-    const int64_t e = (base + s) * a.group + hh;
-    const float ms = a.st_m[e], ls = a.st_l[e];
-    const float4 os = reinterpret_cast<const float4*>(a.st_o + e * D)[ch];
-    const float mn = fmaxf(m, ms);
-    const float a1 = fast_exp2(m - mn), a2 = fast_exp2(ms - mn);
-    l = l * a1 + ls * a2;
-    o.x = o.x * a1 + os.x * a2;
-    o.y = o.y * a1 + os.y * a2;
-    o.z = o.z * a1 + os.z * a2;
-    o.w = o.w * a1 + os.w * a2;
-    m = mn;
-  }
-  __shared__ float s_m[SG], s_l[SG];
-  __shared__ float4 s_o[SG][CH];
-  if (ch == 0) {
-    s_m[sg] = m;
-    s_l[sg] = l;
-  }
-  s_o[sg][ch] = o;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the state has reached memory
   __syncthreads();
-  if (threadIdx.x >= CH) return;
-  m = kLowest;
+  if (threadIdx.x == 0)
+    s_last = __hip_atomic_fetch_add(a.arrivals + pair, 1, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) == ns - 1;
+  __syncthreads();
+  if (!s_last) return;
+  if (threadIdx.x == 0)
+    __hip_atomic_store(a.arrivals + pair, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // Threads take (head, chunk of four channels) and, where there are more
+  // threads than that, a share of the splits each.
+  const int items = G * C4;
+  const int sg_n = items < NW * 64 ? NW * 64 / items : 1;
+  const int64_t first = pair * a.splits;
+  for (int e0 = 0; e0 < items; e0 += NW * 64) {
+    const int e = e0 + threadIdx.x % (sg_n * items);
+    const int item = sg_n > 1 ? e % items : e;
+    const int sg = sg_n > 1 ? e / items : 0;
+    const bool on = sg_n > 1 ? threadIdx.x < sg_n * items : item < items;
+    const int h = item / C4, c4 = item % C4;
+    float m = kLowest, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+      constexpr int U = 8;  // states in flight
+      for (int s0 = sg; s0 < ns; s0 += sg_n * U) {
+        float2 ml[U];
+        float4 os[U];
 #pragma unroll
-  for (int k = 0; k < SG; ++k) m = fmaxf(m, s_m[k]);
-  l = 0.f;
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int u = 0; u < U; ++u) {
+          const int s = min(s0 + u * sg_n, ns - 1);
+          const int64_t at = (first + s) * G + h;
+          ml[u] = get_state2(a.st_ml + at * 2);
+          os[u] = get_state4(a.st_o + at * D + 4 * c4);
+        }
 #pragma unroll
-  for (int k = 0; k < SG; ++k) {
-    const float w = fast_exp2(s_m[k] - m);
-    const float4 v = s_o[k][ch];
-    l = fmaf(w, s_l[k], l);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+        for (int u = 0; u < U; ++u) {
+          if (s0 + u * sg_n < ns) join(m, l, o, ml[u].x, ml[u].y, os[u]);
+        }
+      }
+    }
+    if (sg_n > 1) {  // the shares, in order, through LDS (o of `sh` is read no more)
+      static_assert(sizeof(sh) - offsetof(decltype(sh), o) >= NW * 64 * 24, "room for the shares");
+      float4* s_o = reinterpret_cast<float4*>(&sh.o[0][0][0]);
+      float2* s_ml = reinterpret_cast<float2*>(s_o + NW * 64);
+      if (on) {
+        s_o[threadIdx.x] = o;
+        s_ml[threadIdx.x] = make_float2(m, l);
+      }
+      __syncthreads();
+      if (sg == 0 && on)
+        for (int k = 1; k < sg_n; ++k) {
+          const float2 x = s_ml[threadIdx.x + k * items];
+          join(m, l, o, x.x, x.y, s_o[threadIdx.x + k * items]);
+        }
+    }
+    if (on && sg == 0)
+      write_out<D, BF16>(a, int64_t(row) * a.num_q_heads + g * G + h, c4, m, l, o);
   }
-  const int64_t qh = int64_t(row) * a.num_q_heads + h;
-  const bool none = l == 0.f;
-  const float inv = none ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[ch] =
-      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
-  if (ch == 0 && a.lse) a.lse[qh] = none ? kNegInf : m * kLn2 + __logf(l);
 }
 
 template <int D, bool BF16, bool KV4>
@@ -460,8 +512,6 @@ void launch_gp(const AttendArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 8, 4, PF>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 16, 4, PF>), grid, dim3(256), 0, s, a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((join_kernel<D, BF16>), dim3(a.num_q_heads, a.batch), dim3(256), 0, s, a);
 }
 
 template <int D, bool BF16>

@@ -46,8 +46,7 @@ struct AttendArgs {
   const void* v_pool;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  float* st_m;          // [slots][G], log2 units
-  float* st_l;
+  float* st_ml;         // [slots][G][2]: running max (log2 units) and sum
   float* st_o;          // [slots][G][d]
   int32_t* arrivals;    // [B * Hkv], zero between calls
   void* out;
@@ -61,7 +60,8 @@ struct AttendArgs {
   int32_t splits;
   int32_t window;       // 0: everything
   int32_t sinks;
-  float scale_log2;
+  float scale_log2;     // |scale| log2(e), at least the smallest normal number
+  uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
 };
 
 struct PromptArgs {
@@ -82,7 +82,8 @@ struct PromptArgs {
   int32_t num_pool_pages;
   int32_t window;
   int32_t sinks;
-  float scale_log2;
+  float scale_log2;     // |scale| log2(e), at least the smallest normal number
+  uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
 };
 
 struct StoreArgs {

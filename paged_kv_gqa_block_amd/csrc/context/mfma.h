@@ -82,6 +82,9 @@ __device__ __forceinline__ float sum_x32(float x) {
 // exp2(-inf) = 0 and never meets -inf - -inf.
 constexpr float kLowest = -3.402823466e38f;
 
+// log2 of the largest weight that is kept without moving the running maximum.
+constexpr float kSlack = 8.f;
+
 // A row's length as the operators take it: 0 outside [0, capacity].
 __device__ __forceinline__ int clean_len(int n, int max_pages) {
   return (n < 0 || n > max_pages * 16) ? 0 : n;

@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kKeys = 64;             // keys per step: four pages
 constexpr int kNoPage = 0x7ffffff0;   // token base of an absent page: behind every query
-constexpr float kSlack = 8.f;         // log2 of the largest probability kept without rescaling
 
 // Physical 16-byte chunk of chunk ch of key t.  K is read 32 keys at a time at
 // one chunk, V four keys at a time over 64 bytes: in both, lanes that are
@@ -151,7 +150,7 @@ __device__ __forceinline__ uint2 read_transposed(const void* p) {
 }
 
 template <int D, bool BF16, bool KV4>
-__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles, uint32_t q_flip) {
+__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles) {
   constexpr int NQ = D / 16;  // products over the channels
   constexpr int NC = D / 32;  // channel blocks of the output
   using St = Stage<D, BF16, KV4>;
@@ -208,7 +207,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       qf[t] = mine ? load16(qp + 16 * t) : zero4();
-      qf[t].x ^= q_flip, qf[t].y ^= q_flip, qf[t].z ^= q_flip, qf[t].w ^= q_flip;
+      qf[t].x ^= a.q_flip, qf[t].y ^= a.q_flip, qf[t].z ^= a.q_flip, qf[t].w ^= a.q_flip;
     }
   }
   // Positions of the wave's first and last query (empty when it has none).
@@ -369,33 +368,25 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
 }
 
 template <int D, bool BF16>
-void launch_fmt(bool kv4, const PromptArgs& a, int tiles, uint32_t grid, uint32_t flip,
-                hipStream_t s) {
+void launch_fmt(bool kv4, const PromptArgs& a, int tiles, uint32_t grid, hipStream_t s) {
   if (kv4)
-    hipLaunchKernelGGL((prompt_kernel<D, BF16, true>), dim3(grid), dim3(256), 0, s, a, tiles, flip);
+    hipLaunchKernelGGL((prompt_kernel<D, BF16, true>), dim3(grid), dim3(256), 0, s, a, tiles);
   else
-    hipLaunchKernelGGL((prompt_kernel<D, BF16, false>), dim3(grid), dim3(256), 0, s, a, tiles,
-                       flip);
+    hipLaunchKernelGGL((prompt_kernel<D, BF16, false>), dim3(grid), dim3(256), 0, s, a, tiles);
 }
 
 }  // namespace
 
-pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& args, hipStream_t s) {
-  PromptArgs a = args;
+pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hipStream_t s) {
   const int64_t tiles = prompt_tiles(a);
-  // The kernel takes maxima of unscaled scores, so its scale is positive: a
-  // negative one moves to the queries, and zero becomes the smallest normal
-  // number, which every finite score turns into a weight of exactly 1.
-  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-  a.scale_log2 = __builtin_fmaxf(__builtin_fabsf(a.scale_log2), 1.17549435e-38f);
   const bool bf = p.dtype == PKV_BF16;
   const uint32_t n = static_cast<uint32_t>(tiles * a.num_kv_heads);
   if (p.head_dim == 128) {
-    if (bf) launch_fmt<128, true>(kv4, a, static_cast<int>(tiles), n, flip, s);
-    else launch_fmt<128, false>(kv4, a, static_cast<int>(tiles), n, flip, s);
+    if (bf) launch_fmt<128, true>(kv4, a, static_cast<int>(tiles), n, s);
+    else launch_fmt<128, false>(kv4, a, static_cast<int>(tiles), n, s);
   } else {
-    if (bf) launch_fmt<64, true>(kv4, a, static_cast<int>(tiles), n, flip, s);
-    else launch_fmt<64, false>(kv4, a, static_cast<int>(tiles), n, flip, s);
+    if (bf) launch_fmt<64, true>(kv4, a, static_cast<int>(tiles), n, s);
+    else launch_fmt<64, false>(kv4, a, static_cast<int>(tiles), n, s);
   }
   return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
 }

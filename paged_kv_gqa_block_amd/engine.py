@@ -7,6 +7,7 @@ allocates memory and supplies the stream.
 """
 from __future__ import annotations
 
+import ctypes
 import json
 import os
 
@@ -189,43 +190,71 @@ class _ContextCalls:
         self.dtype = torch.bfloat16 if prob.dtype == _lib.PKV_BF16 else torch.float16
         self.kv4_page_bytes = _context.pkv_kv4_page_bytes(prob.head_dim)
 
-    def _stream(self, stream):
-        return stream if stream is not None else torch.cuda.current_stream(self.device)
+        p = prob
+        self._shapes = {"block_table": (p.batch, p.max_pages_per_row), "seq_lens": (p.batch,),
+                        "tok_offsets": (p.batch + 1,),
+                        "kv4_pool": (p.num_pool_pages, p.num_kv_heads, self.kv4_page_bytes),
+                        "pool": (p.num_pool_pages, p.num_kv_heads, p.page_size, p.head_dim),
+                        "q": (p.batch, p.num_q_heads, p.head_dim)}
+        self._prob_ref = ctypes.byref(prob)
 
-    def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> torch.Tensor:
-        if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device:
+    def _stream(self, stream) -> int:
+        if stream is not None:
+            return stream if isinstance(stream, int) else stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
+        """The address of `t`, after its checks."""
+        if t.shape != shape or t.dtype != dtype or t.device != self.device:
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} "
                              f"{dtype} on {self.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return t
+        return t.data_ptr()
 
-    def _tables(self, block_table, seq_lens) -> None:
-        p = self.prob
-        self._expect("block_table", block_table, (p.batch, p.max_pages_per_row), torch.int32)
-        self._expect("seq_lens", seq_lens, (p.batch,), torch.int32)
+    def _tables(self, block_table, seq_lens) -> tuple:
+        s = self._shapes
+        return (self._expect("block_table", block_table, s["block_table"], torch.int32),
+                self._expect("seq_lens", seq_lens, s["seq_lens"], torch.int32))
 
-    def _offsets(self, tok_offsets, num_tokens: int) -> None:
+    def _offsets(self, tok_offsets, num_tokens: int):
         if tok_offsets is not None:
-            self._expect("tok_offsets", tok_offsets, (self.prob.batch + 1,), torch.int32)
-        elif num_tokens != self.prob.batch:
+            return self._expect("tok_offsets", tok_offsets, self._shapes["tok_offsets"],
+                                torch.int32)
+        if num_tokens != self.prob.batch:
             raise ValueError(f"{num_tokens} tokens of {self.prob.batch} rows need tok_offsets")
+        return None
 
-    def _kv4_pool(self, pool) -> None:
-        p = self.prob
-        self._expect("kv4_pool", pool, (p.num_pool_pages, p.num_kv_heads, self.kv4_page_bytes),
-                     torch.uint8)
+    def _kv4_pool(self, pool) -> int:
+        return self._expect("kv4_pool", pool, self._shapes["kv4_pool"], torch.uint8)
 
     def _pools(self, w: dict) -> tuple:
-        """The cache of `w`: (True, its 4-bit pool) or (False, its two 16-bit pools)."""
-        p = self.prob
+        """The cache of `w`: (its 4-bit pool,) or (its two 16-bit pools)."""
         if "kv4_pool" in w:
-            self._kv4_pool(w["kv4_pool"])
-            return True, w["kv4_pool"]
-        shape = (p.num_pool_pages, p.num_kv_heads, p.page_size, p.head_dim)
-        self._expect("k_pool", w["k_pool"], shape, self.dtype)
-        self._expect("v_pool", w["v_pool"], shape, self.dtype)
-        return False, (w["k_pool"], w["v_pool"])
+            return (self._kv4_pool(w["kv4_pool"]),)
+        shape = self._shapes["pool"]
+        return (self._expect("k_pool", w["k_pool"], shape, self.dtype),
+                self._expect("v_pool", w["v_pool"], shape, self.dtype))
+
+    def _new_tokens(self, name: str, t: torch.Tensor, n: int) -> tuple:
+        """Address and token stride of new keys or values."""
+        p = self.prob
+        if t.shape != (n, p.num_kv_heads, p.head_dim) or t.dtype != self.dtype or \
+                t.device != self.device:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
+        return t.data_ptr(), _context.token_stride(t)
+
+    def _launch(self, fn: str, *args) -> None:
+        """Call an entry point (every argument a number or a reference) with
+        the buffers' device current."""
+        call = getattr(_lib.LIB, fn)
+        if torch.cuda.current_device() == self.device.index:
+            status = call(self._prob_ref, *args)
+        else:
+            with torch.cuda.device(self.device):
+                status = call(self._prob_ref, *args)
+        if status != _lib.PKV_OK:
+            raise _lib.PkvError(fn, status, _lib.pkv_status_str(status))
 
 
 class Kv4Cache(_ContextCalls):
@@ -247,27 +276,20 @@ class Kv4Cache(_ContextCalls):
         """k_new, v_new: [tokens][Hkv][d], heads contiguous, any token stride
         that is a multiple of 8; seq_lens: the lengths after them; tok_offsets:
         [B + 1], or None for one token per row."""
-        p, n = self.prob, k_new.shape[0]
-        for name, t in (("k_new", k_new), ("v_new", v_new)):
-            if (tuple(t.shape) != (n, p.num_kv_heads, p.head_dim) or t.dtype != self.dtype
-                    or t.device != self.device):
-                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
-        self._tables(block_table, seq_lens)
-        self._offsets(tok_offsets, n)
-        with torch.cuda.device(self.device):
-            _context.pkv_kv4_store(p, tok_offsets, n, seq_lens, k_new, v_new, block_table,
-                                   self.pool, self._stream(stream))
+        n = k_new.shape[0]
+        table, lens = self._tables(block_table, seq_lens)
+        self._launch("pkv_kv4_store", self._offsets(tok_offsets, n), n, lens,
+                     *self._new_tokens("k_new", k_new, n), *self._new_tokens("v_new", v_new, n),
+                     table, self.pool.data_ptr(), self._stream(stream))
 
     def load(self, block_table, seq_lens, tok_offsets, k_out, v_out, stream=None) -> tuple:
         """The values the cache stands for, into k_out, v_out [tokens][Hkv][d]."""
         p, n = self.prob, k_out.shape[0]
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            self._expect(name, t, (n, p.num_kv_heads, p.head_dim), self.dtype)
-        self._tables(block_table, seq_lens)
-        self._offsets(tok_offsets, n)
-        with torch.cuda.device(self.device):
-            _context.pkv_kv4_load(p, tok_offsets, n, seq_lens, block_table, self.pool, k_out,
-                                  v_out, self._stream(stream))
+        shape = (n, p.num_kv_heads, p.head_dim)
+        table, lens = self._tables(block_table, seq_lens)
+        self._launch("pkv_kv4_load", self._offsets(tok_offsets, n), n, lens, table,
+                     self.pool.data_ptr(), self._expect("k_out", k_out, shape, self.dtype),
+                     self._expect("v_out", v_out, shape, self.dtype), self._stream(stream))
         return k_out, v_out
 
 
@@ -276,16 +298,11 @@ def store_kv(prob: _lib.pkv_problem, k_new, v_new, block_table, seq_lens, tok_of
     """Write a run of new tokens into the 16-bit pools (arguments as
     ``Kv4Cache.store``)."""
     calls, n = _ContextCalls(prob, k_pool.device), k_new.shape[0]
-    calls._pools({"k_pool": k_pool, "v_pool": v_pool})
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if (tuple(t.shape) != (n, prob.num_kv_heads, prob.head_dim) or t.dtype != calls.dtype
-                or t.device != calls.device):
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
-    calls._tables(block_table, seq_lens)
-    calls._offsets(tok_offsets, n)
-    with torch.cuda.device(calls.device):
-        _context.pkv_store_kv(prob, tok_offsets, n, seq_lens, k_new, v_new, block_table, k_pool,
-                              v_pool, calls._stream(stream))
+    table, lens = calls._tables(block_table, seq_lens)
+    calls._launch("pkv_store_kv", calls._offsets(tok_offsets, n), n, lens,
+                  *calls._new_tokens("k_new", k_new, n), *calls._new_tokens("v_new", v_new, n),
+                  table, *calls._pools({"k_pool": k_pool, "v_pool": v_pool}),
+                  calls._stream(stream))
 
 
 class WindowStep(_ContextCalls):
@@ -298,7 +315,7 @@ class WindowStep(_ContextCalls):
     arguments checked and marshalled once, for loops over fixed buffers.
     """
 
-    _call = "pkv_attend_window"
+    _call, _num_pools = "pkv_attend_window", 2
 
     def __init__(self, prob: _lib.pkv_problem, window: int = 0, sinks: int = 0,
                  splits: int | None = None, device="cuda"):
@@ -317,24 +334,23 @@ class WindowStep(_ContextCalls):
                                device=self.device)
         self.lse = torch.empty(prob.batch, prob.num_q_heads, dtype=torch.float32,
                                device=self.device)
+        self._view_ref = ctypes.byref(self.view)
+        self._own = (self.workspace.data_ptr(), nbytes, self.out.data_ptr(), self.lse.data_ptr())
 
     def bind(self, w: dict, stream=None) -> tuple:
-        p = self.prob
-        self._expect("q", w["q"], (p.batch, p.num_q_heads, p.head_dim), self.dtype)
-        self._tables(w["block_table"], w["seq_lens"])
-        kv4, pools = self._pools(w)
-        if kv4 != (self._call == "pkv_attend_kv4"):
+        q = self._expect("q", w["q"], self._shapes["q"], self.dtype)
+        table, lens = self._tables(w["block_table"], w["seq_lens"])
+        pools = self._pools(w)
+        if len(pools) != self._num_pools:
             raise ValueError(f"{type(self).__name__} over the wrong kind of cache")
-        return _lib.bind_call(self._call, p, self.view, w["seq_lens"], self.splits, w["q"],
-                              *((pools,) if kv4 else pools), w["block_table"], self.workspace,
-                              self.workspace.numel(), self.out, self.lse, self._stream(stream))
+        return (self._view_ref, lens, self.splits, q, *pools, table, *self._own,
+                self._stream(stream))
 
     def run(self, w: dict, stream=None) -> tuple:
         return self.run_bound(self.bind(w, stream))
 
     def run_bound(self, bound: tuple) -> tuple:
-        with torch.cuda.device(self.device):
-            _lib.call_bound(bound)
+        self._launch(self._call, *bound)
         return self.out, self.lse
 
 
@@ -342,7 +358,7 @@ class Kv4Step(WindowStep):
     """One decode step over the 4-bit cache (q, kv4_pool, block_table,
     seq_lens), with the view of ``WindowStep``."""
 
-    _call = "pkv_attend_kv4"
+    _call, _num_pools = "pkv_attend_kv4", 1
 
 
 class PromptStep(_ContextCalls):
@@ -362,24 +378,23 @@ class PromptStep(_ContextCalls):
                                device=self.device)
         self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
                                device=self.device)
+        self._view_ref = ctypes.byref(self.view)
+        self._own = (self.out.data_ptr(), self.lse.data_ptr())
 
     def bind(self, w: dict, stream=None) -> tuple:
-        p, off = self.prob, w.get("tok_offsets")
-        self._expect("q", w["q"], (self.num_tokens, p.num_q_heads, p.head_dim), self.dtype)
-        self._tables(w["block_table"], w["seq_lens"])
-        self._offsets(off, self.num_tokens)
-        kv4, pools = self._pools(w)
-        return _lib.bind_call("pkv_prompt_kv4" if kv4 else "pkv_prompt_window", p, self.view, off,
-                              self.num_tokens, w["seq_lens"], w["q"],
-                              *((pools,) if kv4 else pools), w["block_table"], self.out, self.lse,
-                              self._stream(stream))
+        n = self.num_tokens
+        q = self._expect("q", w["q"], self.out.shape, self.dtype)
+        table, lens = self._tables(w["block_table"], w["seq_lens"])
+        pools = self._pools(w)
+        return ("pkv_prompt_kv4" if len(pools) == 1 else "pkv_prompt_window", self._view_ref,
+                self._offsets(w.get("tok_offsets"), n), n, lens, q, *pools, table, *self._own,
+                self._stream(stream))
 
     def run(self, w: dict, stream=None) -> tuple:
         return self.run_bound(self.bind(w, stream))
 
     def run_bound(self, bound: tuple) -> tuple:
-        with torch.cuda.device(self.device):
-            _lib.call_bound(bound)
+        self._launch(*bound)
         return self.out, self.lse
 
 

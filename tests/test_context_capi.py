@@ -162,9 +162,9 @@ def test_token_strides_are_checked_by_the_binding():
     import torch
 
     x = torch.zeros(4, 2, 3, 64)
-    assert _context._token_stride(x[:, 0]) == 2 * 3 * 64
-    assert _context._token_stride(torch.zeros(1, 3, 64)) == 192
+    assert _context.token_stride(x[:, 0]) == 2 * 3 * 64
+    assert _context.token_stride(torch.zeros(1, 3, 64)) == 192
     with pytest.raises(ValueError):
-        _context._token_stride(x.transpose(1, 2)[:, 0])
+        _context.token_stride(x.transpose(1, 2)[:, 0])
     with pytest.raises(ValueError):
-        _context._token_stride(x[..., ::2][:, 0])
+        _context.token_stride(x[..., ::2][:, 0])
