@@ -137,18 +137,32 @@ int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* view, int32_t
  *   as tok_offsets says (NULL: one token per row, num_tokens = B).
  * P enters the second product rounded to the problem's type; statistics and
  * sums are held in fp32.
- * Errors: PKV_EINVAL, PKV_ESHAPE, PKV_EDTYPE as above, PKV_ERANGE (more than
- * 2^24 - 1 workgroups: (num_tokens * G / 128 + B) * Hkv), PKV_EHIP.
+ *   max_splits: a tile of 128 query rows (tokens times heads of a group) cuts
+ *     its keys into up to this many ranges, for few queries over long contexts;
+ *     1 needs no workspace.  pkv_prompt_splits gives a cap that fills num_cus
+ *     compute units (0 on an invalid argument).
+ *   workspace: pkv_prompt_workspace_bytes device bytes (0 for one split and
+ *     where the call would be refused), on the terms of pkv_attend_window's;
+ *     one_per_row says that the call passes no tok_offsets.
+ * Errors: PKV_EINVAL, PKV_ESHAPE, PKV_EDTYPE, PKV_ENOSPC as above, PKV_ERANGE
+ * (more than 2^24 - 1 workgroups: (num_tokens * G / 128 + B) * Hkv *
+ * max_splits), PKV_EHIP.
  */
+size_t pkv_prompt_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
+                                  int32_t one_per_row, int32_t max_splits);
+int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* view, int32_t num_tokens,
+                          int32_t one_per_row, int32_t num_cus);
 pkv_status pkv_prompt_window(const pkv_problem* prob, const pkv_view* view,
                              const int32_t* tok_offsets, int32_t num_tokens,
-                             const int32_t* seq_lens_dev, const void* q, const void* k_pool,
-                             const void* v_pool, const int32_t* block_table, void* out,
-                             float* lse, hipStream_t stream);
+                             const int32_t* seq_lens_dev, int32_t max_splits, const void* q,
+                             const void* k_pool, const void* v_pool, const int32_t* block_table,
+                             void* workspace, size_t workspace_bytes, void* out, float* lse,
+                             hipStream_t stream);
 pkv_status pkv_prompt_kv4(const pkv_problem* prob, const pkv_view* view,
                           const int32_t* tok_offsets, int32_t num_tokens,
-                          const int32_t* seq_lens_dev, const void* q, const void* kv4_pool,
-                          const int32_t* block_table, void* out, float* lse, hipStream_t stream);
+                          const int32_t* seq_lens_dev, int32_t max_splits, const void* q,
+                          const void* kv4_pool, const int32_t* block_table, void* workspace,
+                          size_t workspace_bytes, void* out, float* lse, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,8 @@ from ._lib import LIB, _check, _ptr, _stream, pkv_problem
 
 EXPORTED = ("pkv_kv4_page_bytes", "pkv_store_kv", "pkv_kv4_store", "pkv_kv4_load",
             "pkv_attend_workspace_bytes", "pkv_attend_window", "pkv_attend_kv4",
-            "pkv_attend_splits", "pkv_prompt_window", "pkv_prompt_kv4")
+            "pkv_attend_splits", "pkv_prompt_workspace_bytes", "pkv_prompt_splits",
+            "pkv_prompt_window", "pkv_prompt_kv4")
 
 
 class pkv_view(ctypes.Structure):
@@ -28,8 +29,12 @@ def _prototypes() -> None:
             ("pkv_attend_window", i32, [prob, view, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp, vp]),
             ("pkv_attend_kv4", i32, [prob, view, vp, i32, vp, vp, vp, vp, sz, vp, vp, vp]),
             ("pkv_attend_splits", i32, [prob, view, i32]),
-            ("pkv_prompt_window", i32, [prob, view, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
-            ("pkv_prompt_kv4", i32, [prob, view, vp, i32, vp, vp, vp, vp, vp, vp, vp])):
+            ("pkv_prompt_workspace_bytes", sz, [prob, i32, i32, i32]),
+            ("pkv_prompt_splits", i32, [prob, view, i32, i32, i32]),
+            ("pkv_prompt_window", i32,
+             [prob, view, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp, vp]),
+            ("pkv_prompt_kv4", i32,
+             [prob, view, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp, vp, vp])):
         # A host-only build named by PKV_LIBRARY may hold the decode engine
         # alone; a call of a missing entry point then fails by its name.
         if hasattr(LIB, name):
@@ -107,16 +112,26 @@ def pkv_attend_kv4(prob, view, seq_lens_dev, max_splits: int, q, kv4_pool, block
         _stream(stream)))
 
 
-def pkv_prompt_window(prob, view, tok_offsets, num_tokens: int, seq_lens_dev, q, k_pool, v_pool,
-                      block_table, out, lse=None, stream=None) -> None:
+def pkv_prompt_workspace_bytes(prob, num_tokens: int, one_per_row: bool, max_splits: int) -> int:
+    return LIB.pkv_prompt_workspace_bytes(ctypes.byref(prob), num_tokens, one_per_row, max_splits)
+
+
+def pkv_prompt_splits(prob, view, num_tokens: int, one_per_row: bool, num_cus: int) -> int:
+    return LIB.pkv_prompt_splits(ctypes.byref(prob), _byref(view), num_tokens, one_per_row,
+                                 num_cus)
+
+
+def pkv_prompt_window(prob, view, tok_offsets, num_tokens: int, seq_lens_dev, max_splits: int, q,
+                      k_pool, v_pool, block_table, workspace, out, lse=None, stream=None) -> None:
     _check("pkv_prompt_window", LIB.pkv_prompt_window(
         ctypes.byref(prob), _byref(view), _ptr(tok_offsets), num_tokens, _ptr(seq_lens_dev),
-        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(out), _ptr(lse),
-        _stream(stream)))
+        max_splits, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _ptr(out), _ptr(lse), _stream(stream)))
 
 
-def pkv_prompt_kv4(prob, view, tok_offsets, num_tokens: int, seq_lens_dev, q, kv4_pool,
-                   block_table, out, lse=None, stream=None) -> None:
+def pkv_prompt_kv4(prob, view, tok_offsets, num_tokens: int, seq_lens_dev, max_splits: int, q,
+                   kv4_pool, block_table, workspace, out, lse=None, stream=None) -> None:
     _check("pkv_prompt_kv4", LIB.pkv_prompt_kv4(
         ctypes.byref(prob), _byref(view), _ptr(tok_offsets), num_tokens, _ptr(seq_lens_dev),
-        _ptr(q), _ptr(kv4_pool), _ptr(block_table), _ptr(out), _ptr(lse), _stream(stream)))
+        max_splits, _ptr(q), _ptr(kv4_pool), _ptr(block_table), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _ptr(out), _ptr(lse), _stream(stream)))

@@ -25,6 +25,7 @@
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
+#include "states.h"
 
 namespace pkv {
 namespace {
@@ -46,29 +47,7 @@ template <int D, bool KV4>
 struct PageRegs;
 
 template <int D>
-struct PageRegs<D, true> {
-  uint32_t k[D / 32], v[D / 32];
-  uint32_t ks, vs;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane) {
-    const int kg = lane >> 4, c = lane & 15;
-    if constexpr (D == 128) {
-      const uint4 x = buffer_load16(r, lane * 16), y = buffer_load16(r, Kv4<D>::kV + lane * 16);
-      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
-      v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-      ks = __builtin_amdgcn_raw_buffer_load_b32(r, Kv4<D>::kKs + c * 4, 0, kCachePolicyStream);
-    } else {
-      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, 0, kCachePolicyStream);
-      const auto y = __builtin_amdgcn_raw_buffer_load_b64(r, Kv4<D>::kV + lane * 8, 0,
-                                                          kCachePolicyStream);
-      k[0] = x[0], k[1] = x[1];
-      v[0] = y[0], v[1] = y[1];
-      ks = __builtin_amdgcn_raw_buffer_load_b16(r, Kv4<D>::kKs + c * 2, 0, kCachePolicyStream);
-    }
-    // The lane's V channels lie in one block.
-    vs = __builtin_amdgcn_raw_buffer_load_b32(
-        r, Kv4<D>::kVs + kg * (D / 8) + (c / (512 / D)) * 4, 0, kCachePolicyStream);
-  }
-};
+struct PageRegs<D, true> : Kv4Page<D> {};
 
 template <int D>
 struct PageRegs<D, false> {
@@ -115,27 +94,6 @@ __device__ __forceinline__ int ktile_chunk(int t, int ch) {
     return ch ^ (((t & 3) << 2) | (t >> 2));
   else
     return ch ^ (((t & 3) << 1) | ((t >> 2) & 1));
-}
-
-// Partial states cross from one XCD's L2 to another's inside a launch: stores
-// and loads at agent scope pass through both.
-__device__ __forceinline__ void put_state(float* p, float x, float y) {
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p),
-                     __builtin_bit_cast(uint64_t, make_float2(x, y)), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void put_state(float* p, const float4& o) {
-  put_state(p, o.x, o.y);
-  put_state(p + 2, o.z, o.w);
-}
-__device__ __forceinline__ float2 get_state2(const float* p) {
-  return __builtin_bit_cast(
-      float2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                __HIP_MEMORY_SCOPE_AGENT));
-}
-__device__ __forceinline__ float4 get_state4(const float* p) {
-  const float2 a = get_state2(p), b = get_state2(p + 2);
-  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // (m, l, o) joined with (m1, l1, o1).
@@ -242,10 +200,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3,8))) 
       if constexpr (KV4) {
         const uint8_t* p = static_cast<const uint8_t*>(a.k_pool) +
                            (int64_t(max(id, 0)) * hkv + g) * Kv4<D>::kBytes;
-        u.page[x].load(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0,
-                                                         id >= 0 ? Kv4<D>::kBytes : 0,
-                                                         kBufferFlags),
-                       lane);
+        const auto r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(p), (short)0, id >= 0 ? Kv4<D>::kBytes : 0, kBufferFlags);
+        u.page[x].template load_k<kCachePolicyStream>(r, lane);
+        u.page[x].template load_v<kCachePolicyStream>(r, lane);
       } else {
         // Tokens past the row's length are not fetched: they read as zero.
         const int base = table_index(page_of(k0 + j) + x) * 16;
@@ -442,15 +400,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3,8))) 
   // Its sum runs in split order, so the result does not depend on who arrives
   // last.  M = max m_s, w_s = 2^(m_s - M), out = sum w_s o_s / sum w_s l_s.
   const int ns = (sp.count + pps - 1) / pps;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the state has reached memory
-  __syncthreads();
-  if (threadIdx.x == 0)
-    s_last = __hip_atomic_fetch_add(a.arrivals + pair, 1, __ATOMIC_RELAXED,
-                                    __HIP_MEMORY_SCOPE_AGENT) == ns - 1;
-  __syncthreads();
-  if (!s_last) return;
-  if (threadIdx.x == 0)
-    __hip_atomic_store(a.arrivals + pair, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (!last_to_arrive(a.arrivals + pair, ns, &s_last)) return;
   // Threads take (head, chunk of four channels) and, where there are more
   // threads than that, a share of the splits each.
   const int items = G * C4;

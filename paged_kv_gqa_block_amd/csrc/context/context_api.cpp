@@ -126,17 +126,33 @@ pkv_status attend(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   return launch_attend(*prob, kv4, a, stream);
 }
 
+// Workspace of a split prompt: arrivals, then the states.
+struct PromptWorkspace {
+  size_t state, bytes;
+};
+
+PromptWorkspace prompt_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits) {
+  const size_t pairs = static_cast<size_t>(tiles) * p->num_kv_heads;
+  PromptWorkspace w;
+  w.state = (pairs * sizeof(int32_t) + 255) & ~size_t(255);
+  w.bytes = w.state + pairs * splits * prompt_state_floats(p->head_dim) * sizeof(float);
+  return w;
+}
+
 pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* tok_offsets,
-                  int32_t num_tokens, const int32_t* seq_lens, const void* q, bool kv4,
-                  const void* k_pool, const void* v_pool, const int32_t* block_table, void* out,
-                  float* lse, hipStream_t stream) {
+                  int32_t num_tokens, const int32_t* seq_lens, int32_t max_splits, const void* q,
+                  bool kv4, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                  void* workspace, size_t workspace_bytes, void* out, float* lse,
+                  hipStream_t stream) {
   pkv_status st = check_run(prob, tok_offsets, num_tokens, seq_lens, block_table);
   if (st != PKV_OK) return st;
   st = check_view(view);
   if (st != PKV_OK) return st;
+  if (max_splits < 1 || max_splits > 65535) return PKV_EINVAL;
   if (num_tokens == 0) return PKV_OK;
-  if (!q || !k_pool || (!kv4 && !v_pool) || !out) return PKV_EINVAL;
-  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+  if (!q || !k_pool || (!kv4 && !v_pool) || !out || (max_splits > 1 && !workspace))
+    return PKV_EINVAL;
+  if (!aligned(workspace, 16) || !aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
     return PKV_ESHAPE;
   PromptArgs a{};
   a.q = q;
@@ -157,7 +173,15 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   a.window = clean_window(prob, view);
   a.sinks = view ? view->sinks : 0;
   set_scale(prob, &a);
-  if (prompt_tiles(a) * a.num_kv_heads > kMaxGridGroups) return PKV_ERANGE;
+  a.splits = max_splits;
+  const int64_t tiles = prompt_tiles(a);
+  if (tiles * a.num_kv_heads * max_splits > kMaxGridGroups) return PKV_ERANGE;
+  if (max_splits > 1) {
+    const PromptWorkspace w = prompt_workspace_of(prob, tiles, max_splits);
+    if (workspace_bytes < w.bytes) return PKV_ENOSPC;
+    a.arrivals = static_cast<int32_t*>(workspace);
+    a.state = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.state);
+  }
   return launch_prompt(*prob, kv4, a, stream);
 }
 
@@ -287,19 +311,56 @@ extern "C" pkv_status pkv_attend_kv4(const pkv_problem* prob, const pkv_view* vi
 
 extern "C" pkv_status pkv_prompt_window(const pkv_problem* prob, const pkv_view* view,
                                         const int32_t* tok_offsets, int32_t num_tokens,
-                                        const int32_t* seq_lens_dev, const void* q,
-                                        const void* k_pool, const void* v_pool,
-                                        const int32_t* block_table, void* out, float* lse,
+                                        const int32_t* seq_lens_dev, int32_t max_splits,
+                                        const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* block_table, void* workspace,
+                                        size_t workspace_bytes, void* out, float* lse,
                                         hipStream_t stream) {
-  return prompt(prob, view, tok_offsets, num_tokens, seq_lens_dev, q, false, k_pool, v_pool,
-                block_table, out, lse, stream);
+  return prompt(prob, view, tok_offsets, num_tokens, seq_lens_dev, max_splits, q, false, k_pool,
+                v_pool, block_table, workspace, workspace_bytes, out, lse, stream);
 }
 
 extern "C" pkv_status pkv_prompt_kv4(const pkv_problem* prob, const pkv_view* view,
                                      const int32_t* tok_offsets, int32_t num_tokens,
-                                     const int32_t* seq_lens_dev, const void* q,
-                                     const void* kv4_pool, const int32_t* block_table, void* out,
-                                     float* lse, hipStream_t stream) {
-  return prompt(prob, view, tok_offsets, num_tokens, seq_lens_dev, q, true, kv4_pool, nullptr,
-                block_table, out, lse, stream);
+                                     const int32_t* seq_lens_dev, int32_t max_splits,
+                                     const void* q, const void* kv4_pool,
+                                     const int32_t* block_table, void* workspace,
+                                     size_t workspace_bytes, void* out, float* lse,
+                                     hipStream_t stream) {
+  return prompt(prob, view, tok_offsets, num_tokens, seq_lens_dev, max_splits, q, true, kv4_pool,
+                nullptr, block_table, workspace, workspace_bytes, out, lse, stream);
+}
+
+namespace {
+
+// Query tiles of a run batch, from the host's numbers alone; -1 when invalid.
+int64_t tiles_of(const pkv_problem* p, int32_t num_tokens, int32_t one_per_row) {
+  if (check_problem(p) != PKV_OK || num_tokens < 0 || (one_per_row && num_tokens != p->batch))
+    return -1;
+  return one_per_row ? p->batch
+                     : tile_base(num_tokens, p->batch, p->num_q_heads / p->num_kv_heads);
+}
+
+}  // namespace
+
+extern "C" size_t pkv_prompt_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
+                                             int32_t one_per_row, int32_t max_splits) {
+  const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
+  if (tiles < 0 || max_splits < 1 || max_splits > 65535 ||
+      tiles * prob->num_kv_heads * max_splits > kMaxGridGroups || max_splits == 1)
+    return 0;
+  return prompt_workspace_of(prob, tiles, max_splits).bytes;
+}
+
+extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* view,
+                                     int32_t num_tokens, int32_t one_per_row, int32_t num_cus) {
+  const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
+  if (tiles < 0 || check_view(view) != PKV_OK || num_cus < 1 || num_cus > 1024) return 0;
+  if (tiles == 0) return 1;
+  // Two workgroups a compute unit, as long as a split keeps eight steps of four
+  // pages.
+  const int64_t fill = 2 * int64_t(num_cus) / (tiles * prob->num_kv_heads);
+  const int64_t keys = std::min<int64_t>(most_pages(prob, view) + ceil_div(num_tokens, 16),
+                                         prob->max_pages_per_row);
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min(fill, keys / 32)));
 }

@@ -71,6 +71,8 @@ struct PromptArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* tok_offsets;  // [B + 1]
+  float* state;         // splits' states, see prompt.hip
+  int32_t* arrivals;    // [tiles * Hkv], zero between calls
   void* out;
   float* lse;
   int32_t batch;
@@ -80,6 +82,7 @@ struct PromptArgs {
   int32_t group;
   int32_t max_pages;
   int32_t num_pool_pages;
+  int32_t splits;
   int32_t window;
   int32_t sinks;
   float scale_log2;     // |scale| log2(e), at least the smallest normal number
@@ -134,6 +137,8 @@ constexpr int kTileRows = 128;
 PKV_HD int64_t tile_base(int64_t off, int64_t row, int group) {
   return off * group / kTileRows + row;
 }
+// Floats of one split's state of one tile and KV head (prompt.hip).
+inline size_t prompt_state_floats(int head_dim) { return 256 * (size_t(head_dim) / 2 + 2); }
 inline int64_t prompt_tiles(const PromptArgs& a) {
   return a.tok_offsets ? tile_base(a.num_tokens, a.batch, a.group) : int64_t(a.batch);
 }

@@ -64,4 +64,38 @@ __device__ __forceinline__ uint4 kv4_eight(uint32_t w, float scale) {
                     kv4_pair<BF16, 2>(w, scale), kv4_pair<BF16, 3>(w, scale));
 }
 
+// One page of one KV head as a wave holds it (the lane's pieces above).
+template <int D>
+struct Kv4Page {
+  uint32_t k[D / 32], v[D / 32];
+  uint32_t ks, vs;
+  template <int POLICY>
+  __device__ __forceinline__ void load_k(__amdgpu_buffer_rsrc_t r, int lane) {
+    const int c = lane & 15;
+    if constexpr (D == 128) {
+      const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, lane * 16, 0, POLICY);
+      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+      ks = __builtin_amdgcn_raw_buffer_load_b32(r, Kv4<D>::kKs + c * 4, 0, POLICY);
+    } else {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, lane * 8, 0, POLICY);
+      k[0] = x[0], k[1] = x[1];
+      ks = __builtin_amdgcn_raw_buffer_load_b16(r, Kv4<D>::kKs + c * 2, 0, POLICY);
+    }
+  }
+  template <int POLICY>
+  __device__ __forceinline__ void load_v(__amdgpu_buffer_rsrc_t r, int lane) {
+    const int kg = lane >> 4, c = lane & 15;
+    if constexpr (D == 128) {
+      const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, Kv4<D>::kV + lane * 16, 0, POLICY);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, Kv4<D>::kV + lane * 8, 0, POLICY);
+      v[0] = x[0], v[1] = x[1];
+    }
+    // The lane's V channels lie in one block.
+    vs = __builtin_amdgcn_raw_buffer_load_b32(
+        r, Kv4<D>::kVs + kg * (D / 8) + (c / (512 / D)) * 4, 0, POLICY);
+  }
+};
+
 }  // namespace pkv

@@ -8,26 +8,34 @@
 // Bound: the matrix core, 4 d flops per visible (query, key).  A workgroup owns
 // 128 packed query rows (token-major, the G heads of a KV head side by side, so
 // that they share its keys) and walks the pages that any of them sees, 64 keys
-// at a time through two LDS buffers; each of its four waves owns 32 rows.
+// a step through two LDS buffers; each of its four waves owns 32 rows.  Few
+// tiles over many keys are cut along the keys (splits), and the last split of
+// a tile to finish joins the partial states.
 //  * S^T = K Q^T on v_mfma_f32_32x32x16: a lane holds one query's scores for 16
 //    of 32 keys, so maximum and sum need one exchange with the lane 32 away.
 //  * O^T += V^T P^T: the lane's own probabilities are the B operand as they
 //    stand (the order of the keys inside a product is free), and V^T comes out
 //    of row-major LDS by the transposing read ds_read_b64_tr_b16.
+//  * The next step's scores are started before this step's softmax, so that the
+//    matrix core works while the vector unit does.
+//  * 16-bit pages go to LDS directly (buffer_load ... lds); wave w brings page w
+//    of the step.
 //  * O is rescaled only when a score passes the running maximum by more than
-//    2^8: below that, exp2 stays exact enough in fp32 and fits in f16.
+//    2^8 (kSlack).
 // The probabilities enter the second product rounded to the problem's type (a
-// relative 2^-9 (bf16) or 2^-12 (f16) each, of the size of the output's own
-// rounding); maxima, sums and outputs are fp32 until the last rounding.
+// relative 2^-8 (bf16) or 2^-11 (f16) at most each, of the size of the output's
+// own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
+// last rounding.
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
 #include "runs.h"
+#include "states.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kKeys = 64;             // keys per step: four pages
+constexpr int kKeys = 64;             // keys per step: four pages, one per wave
 constexpr int kNoPage = 0x7ffffff0;   // token base of an absent page: behind every query
 
 // Physical 16-byte chunk of chunk ch of key t.  K is read 32 keys at a time at
@@ -42,132 +50,49 @@ __device__ __forceinline__ int v_chunk(int t, int ch) {
   return D == 128 ? ch ^ ((t & 3) << 2) : ch ^ (((t >> 1) & 1) << 2);
 }
 
-template <int D>
-struct PromptShared {
-  uint4 k[2][kKeys][D / 8];
-  uint4 v[2][kKeys][D / 8];
-};
-
-// Token bases of the four pages of a step (kNoPage where there is none).
-struct Pages {
-  int base[4];
-};
-
-// One step's keys and values on their way to LDS.  Load x covers pages x (d =
-// 128) or 2 x and 2 x + 1 (d = 64, one for each half of the workgroup).
-template <int D, bool BF16, bool KV4>
-struct Stage {
-  static constexpr int NL = D / 32;
-  uint4 k[KV4 ? 1 : NL], v[KV4 ? 1 : NL];
-  uint32_t ck[KV4 ? NL : 1], cv[KV4 ? NL : 1], sk[KV4 ? NL : 1], sv[KV4 ? NL : 1];
-
-  static __device__ __forceinline__ int page(int x, int wave) {
-    return D == 128 ? x : 2 * x + (wave >> 1);
-  }
-  // Thread's index among those of its page.
-  static __device__ __forceinline__ int slot(int tid) { return D == 128 ? tid : tid & 127; }
-
-  // `id`: this load's pool page or -1; `len - base` tokens of it exist.
-  __device__ __forceinline__ void load(int x, const PromptArgs& a, int g, int id, int left,
-                                       int tid) {
-    const int u = slot(tid);
-    const int64_t at = int64_t(max(id, 0)) * a.num_kv_heads + g;
-    if constexpr (KV4) {
-      const uint8_t* p = static_cast<const uint8_t*>(a.k_pool) + at * Kv4<D>::kBytes;
-      const auto r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(p), (short)0, id >= 0 ? Kv4<D>::kBytes : 0, kBufferFlags);
-      const int l = u / (D / 32), w = u % (D / 32);  // lane piece and dword of it
-      const int kg = l >> 4, c = l & 15;
-      ck[x] = __builtin_amdgcn_raw_buffer_load_b32(r, u * 4, 0, 0);
-      cv[x] = __builtin_amdgcn_raw_buffer_load_b32(r, Kv4<D>::kV + u * 4, 0, 0);
-      sk[x] = __builtin_amdgcn_raw_buffer_load_b8(r, Kv4<D>::ks_at(c, w), 0, 0);
-      if constexpr (D == 128)
-        sv[x] = __builtin_amdgcn_raw_buffer_load_b8(r, Kv4<D>::vs_at(4 * kg + w, c >> 2), 0, 0);
-      else
-        sv[x] = __builtin_amdgcn_raw_buffer_load_b16(r, Kv4<D>::vs_at(4 * kg + 2 * w, c >> 3), 0,
-                                                     0);
-    } else {
-      const int bytes = id >= 0 ? min(16, left) * D * 2 : 0;
-      const uint16_t* kp = static_cast<const uint16_t*>(a.k_pool) + at * 16 * D;
-      const uint16_t* vp = static_cast<const uint16_t*>(a.v_pool) + at * 16 * D;
-      const auto kr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(kp), (short)0, bytes,
-                                                        kBufferFlags);
-      const auto vr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(vp), (short)0, bytes,
-                                                        kBufferFlags);
-      const u32x4 kk = __builtin_amdgcn_raw_buffer_load_b128(kr, u * 16, 0, 0);
-      const u32x4 vv = __builtin_amdgcn_raw_buffer_load_b128(vr, u * 16, 0, 0);
-      k[x] = make_uint4(kk.x, kk.y, kk.z, kk.w);
-      v[x] = make_uint4(vv.x, vv.y, vv.z, vv.w);
-    }
-  }
-
-  // To LDS.  seen(t): whether some query of the tile sees token t of the page;
-  // the others' V is cleared, because 0 * NaN is not 0.
-  template <typename Seen>
-  __device__ __forceinline__ void put(int x, PromptShared<D>& sh, int buf, int tid, int wave,
-                                      bool all_seen, Seen seen) {
-    const int u = slot(tid), key0 = 16 * page(x, wave);
-    if constexpr (KV4) {
-      const int l = u / (D / 32), w = u % (D / 32);
-      const int kg = l >> 4, c = l & 15;
-      sh.k[buf][key0 + c][k_chunk<D>(key0 + c, 4 * w + kg)] =
-          kv4_eight<BF16>(ck[x], kv4_scale(sk[x]));
-      if constexpr (D == 128) {
-        const int t = 4 * kg + w;
-        uint4 e = kv4_eight<BF16>(cv[x], kv4_scale(sv[x]));
-        if (!all_seen && !seen(t)) e = zero4();
-        sh.v[buf][key0 + t][v_chunk<D>(key0 + t, c)] = e;
-      } else {
-        const int t = 4 * kg + 2 * w;
-        const float s0 = kv4_scale(sv[x] & 0xff), s1 = kv4_scale((sv[x] >> 8) & 0xff);
-        uint2 e0 = make_uint2(kv4_pair<BF16, 0>(cv[x], s0), kv4_pair<BF16, 1>(cv[x], s0));
-        uint2 e1 = make_uint2(kv4_pair<BF16, 2>(cv[x], s1), kv4_pair<BF16, 3>(cv[x], s1));
-        if (!all_seen && !seen(t)) e0 = make_uint2(0u, 0u);
-        if (!all_seen && !seen(t + 1)) e1 = make_uint2(0u, 0u);
-        reinterpret_cast<uint2*>(&sh.v[buf][key0 + t][v_chunk<D>(key0 + t, c >> 1)])[c & 1] = e0;
-        reinterpret_cast<uint2*>(&sh.v[buf][key0 + t + 1][v_chunk<D>(key0 + t + 1, c >> 1)])[c & 1] =
-            e1;
-      }
-    } else {
-      const int t = u / (D / 8), c = u % (D / 8);
-      sh.k[buf][key0 + t][k_chunk<D>(key0 + t, c)] = k[x];
-      uint4 e = v[x];
-      if (!all_seen && !seen(t)) e = zero4();
-      sh.v[buf][key0 + t][v_chunk<D>(key0 + t, c)] = e;
-    }
-  }
-};
-
+typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+// 16 bytes a lane from a buffer to LDS, in lane order from p on.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* p, uint32_t lane_offset,
+                                           uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)p, 16, lane_offset, offset, 0, 0);
+}
 
 // Four keys by 16 channels per 16 lanes, transposed: lane a of the 16 passes
 // the address of key a / 4, channels 4 (a % 4) .., and gets channel a of the
 // four keys.
 __device__ __forceinline__ uint2 read_transposed(const void* p) {
-  return __builtin_bit_cast(
-      uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                 (lds_bf16x4*)(__attribute__((address_space(3))) void*)(const_cast<void*>(p))));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (lds_bf16x4*)(lds_void*)(const_cast<void*>(p))));
 }
 
 template <int D, bool BF16, bool KV4>
 __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles) {
-  constexpr int NQ = D / 16;  // products over the channels
-  constexpr int NC = D / 32;  // channel blocks of the output
-  using St = Stage<D, BF16, KV4>;
-  __shared__ PromptShared<D> sh;
+  constexpr int NQ = D / 16;   // products over the channels
+  constexpr int NC = D / 32;   // channel blocks of the output
+  constexpr int CH = D / 8;    // 16-byte chunks of a key
+  constexpr int KPL = 64 / CH; // keys of one 1 KiB load
+  constexpr int NL = 16 / KPL; // loads of a page
+  // Objects of their own, named at compile time where they are used: the
+  // compiler then knows which loads to LDS a read has to wait for.
+  using Tile = uint4[kKeys][CH];
+  __shared__ Tile kt0, kt1, vt0, vt1;
+  __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
   const int g = blockIdx.x % a.num_kv_heads;
+  const int ts = blockIdx.x / a.num_kv_heads;
+  const int split = ts % a.splits;
   // Late tiles of a causal row see the most keys: they start first.
-  const int item = tiles - 1 - static_cast<int>(blockIdx.x / a.num_kv_heads);
+  const int item = tiles - 1 - ts / a.splits;
   const int G = a.group;
 
   int row = item, k_tile = 0;
   if (a.tok_offsets) {
-    row = find_row(a.tok_offsets, a.batch, a.num_tokens, item, [&](int64_t off, int64_t r) {
-      return tile_base(off, r, G);
-    });
+    row = find_row(a.tok_offsets, a.batch, a.num_tokens, item,
+                   [&](int64_t off, int64_t r) { return tile_base(off, r, G); });
   }
   const Run run = run_of(a.tok_offsets, a.seq_lens, row, a.num_tokens, a.max_pages);
   if (a.tok_offsets) k_tile = item - static_cast<int>(tile_base(run.first, row, G));
@@ -189,15 +114,19 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const bool mine = my < rows;
 
   if (p_last < 0) {  // no query of the tile is at a position of the row
-    if (mine) {
+    if (mine && split == 0) {
       for (int e = h; e < D / 4; e += 2)
         reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[e] = make_uint2(0u, 0u);
       if (a.lse && h == 0) a.lse[qh] = kNegInf;
     }
     return;
   }
+  const int window = a.window > 0 ? a.window : 0x7fffffff;
   const SeenPages sp = seen_pages(p_first, p_last, a.window, a.sinks);
-  const int steps = (sp.count + 3) >> 2;
+  const int all_steps = (sp.count + 3) >> 2;
+  const int per_split = (all_steps + a.splits - 1) / a.splits;
+  const int s_begin = split * per_split, s_end = min(s_begin + per_split, all_steps);
+  if (s_begin >= s_end) return;
   const int32_t* bt = a.block_table + int64_t(row) * a.max_pages;
 
   // B operand of the scores: channels 16 t + 8 h .. of this lane's query.
@@ -210,49 +139,128 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
       qf[t].x ^= a.q_flip, qf[t].y ^= a.q_flip, qf[t].z ^= a.q_flip, qf[t].w ^= a.q_flip;
     }
   }
-  // Positions of the wave's first and last query (empty when it has none).
-  const bool busy = wr < rows;
+  // Steps whose every key is seen by every query of the wave (absent pages
+  // aside): those behind the start of the last query's window and before the
+  // first query's position, or those before the end of the sinks.
   const int pw_first = max(shift + (r0 + min(wr, rows - 1)) / G, -1);
   const int pw_last = max(shift + (r0 + min(wr + 31, rows - 1)) / G, -1);
+  int full_lo = 0;
+  if (a.window > 0) {
+    const int w0 = max(pw_last - a.window + 1, 0);           // first token all of them see
+    full_lo = (max(((w0 + 15) >> 4) - sp.skip, sp.ahead) + 3) >> 2;
+  }
+  const int full_hi = (((pw_first + 1) >> 4) - sp.skip) >> 2;  // pages that end by pw_first
+  const int sink_hi = min(min(a.sinks, pw_first + 1) >> 4, sp.ahead) >> 2;
 
-  // ---- staging ----------------------------------------------------------------
-  St st;
-  Pages next;  // of the step in `st`
-  int ids = -1;
-  auto issue = [&](int s) {
-    if ((s & 15) == 0) {  // pool pages of 16 steps, one per lane
-      const int v = 4 * s + lane;
-      const int id = v < sp.count ? bt[v < sp.ahead ? v : v + sp.skip] : -1;
-      ids = (static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pool_pages)) ? id : -1;
-    }
-    int id[4];
+  // ---- bringing pages to LDS: wave w brings page w of a step -----------------------
+  // Pool pages of 16 steps, one per lane; -1 where there is none.
+  auto load_ids = [&](int s0) {
+    const int v = 4 * s0 + lane;
+    const int id = v < sp.count ? bt[v < sp.ahead ? v : v + sp.skip] : -1;
+    return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pool_pages) ? id : -1;
+  };
+  auto base_of = [&](int s) {
+    const int v = 4 * s + wave;
+    return 16 * (v < sp.ahead ? v : v + sp.skip);
+  };
+  // Offset of a lane's 16 bytes in its page, load by load, so that they land
+  // where k_chunk and v_chunk say: LDS is filled in lane order.
+  uint32_t k_off[NL];
+  const int lk = lane / CH, lc = lane % CH;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int v = 4 * s + x;
-      id[x] = __builtin_amdgcn_readlane(ids, v & 63);
-      next.base[x] = id[x] >= 0 ? 16 * (v < sp.ahead ? v : v + sp.skip) : kNoPage;
-    }
+  for (int i = 0; i < NL; ++i)
+    k_off[i] = ((KPL * i + lk) * CH + k_chunk<D>(KPL * i + lk, lc)) * 16;
+  const uint32_t v_off = (lk * CH + v_chunk<D>(lk, lc)) * 16;
+  auto rsrc = [&](const void* pool, int id, int bytes) {
+    bytes = __builtin_amdgcn_readfirstlane(bytes);
+    const int64_t at = (int64_t(max(id, 0)) * a.num_kv_heads + g) * 32 * D;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(pool)) + at, (short)0, bytes, kBufferFlags);
+  };
+  // Bytes of a page up to the last token that some query sees: behind them
+  // loads give zero.
+  auto seen_bytes = [&](int id, int s) {
+    return id < 0 ? 0 : min(max(p_last + 1 - base_of(s), 0), 16) * 2 * D;
+  };
+  Kv4Page<D> k4, v4;  // 4-bit: a step's page on its way (K and V travel a step apart)
+  auto rsrc4 = [&](int id) {
+    const int64_t at = (int64_t(max(id, 0)) * a.num_kv_heads + g) * Kv4<D>::kBytes;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(a.k_pool)) + at, (short)0,
+        id >= 0 ? Kv4<D>::kBytes : 0, kBufferFlags);
+  };
+  auto issue_k = [&](int id, int s, Tile& kt) __attribute__((always_inline)) {
+    if constexpr (KV4) {
+      k4.template load_k<0>(rsrc4(id), lane);
+    } else {
+      const auto r = rsrc(a.k_pool, id, seen_bytes(id, s));
 #pragma unroll
-    for (int x = 0; x < St::NL; ++x) {
-      // Selected without an index into registers.
-      const int i0 = D == 128 ? id[x] : (wave >> 1) ? id[2 * x + 1] : id[2 * x];
-      const int b0 = D == 128 ? next.base[x] : (wave >> 1) ? next.base[2 * x + 1] : next.base[2 * x];
-      st.load(x, a, g, i0, run.len - b0, tid);
+      for (int i = 0; i < NL; ++i)
+        load_lds16(r, &kt[16 * wave + KPL * i][0], k_off[i], 0);
     }
   };
-  auto put = [&](int buf) {
+  auto issue_v = [&](int id, int s, Tile& vt) __attribute__((always_inline)) {
+    if constexpr (KV4) {
+      v4.template load_v<0>(rsrc4(id), lane);
+    } else {
+      const auto r = rsrc(a.v_pool, id, seen_bytes(id, s));
 #pragma unroll
-    for (int x = 0; x < St::NL; ++x) {
-      const int b0 = D == 128 ? next.base[x] : (wave >> 1) ? next.base[2 * x + 1] : next.base[2 * x];
-      const bool all_seen = b0 + 15 <= p_last && (a.window == 0 || b0 > p_first - a.window ||
-                                                  b0 + 15 < a.sinks);
-      st.put(x, sh, buf, tid, wave, all_seen, [&](int t) {
-        return b0 + t <= p_last &&
-               (a.window == 0 || b0 + t > p_first - a.window || b0 + t < a.sinks);
-      });
+      for (int i = 0; i < NL; ++i)
+        load_lds16(r, &vt[16 * wave + KPL * i][0], v_off, i * 1024);
+    }
+  };
+  // 4-bit: to LDS, converted.
+  auto put_k = [&](Tile& kt) __attribute__((always_inline)) {
+    if constexpr (KV4) {
+      const int kg = lane >> 4, t = 16 * wave + (lane & 15);
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b)
+        kt[t][k_chunk<D>(t, 4 * b + kg)] =
+            kv4_eight<BF16>(k4.k[b], kv4_scale((k4.ks >> (8 * b)) & 0xff));
+    }
+  };
+  auto put_v = [&](Tile& vt) __attribute__((always_inline)) {
+    if constexpr (KV4) {
+      const int c = lane & 15;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * wave + 4 * (lane >> 4) + i;
+        const float sc = kv4_scale((v4.vs >> (8 * i)) & 0xff);
+        if constexpr (D == 128) {
+          vt[t][v_chunk<D>(t, c)] = kv4_eight<BF16>(v4.v[i], sc);
+        } else {
+          const uint32_t two = v4.v[i >> 1];
+          reinterpret_cast<uint2*>(&vt[t][v_chunk<D>(t, c >> 1)])[c & 1] =
+              (i & 1) ? make_uint2(kv4_pair<BF16, 2>(two, sc), kv4_pair<BF16, 3>(two, sc))
+                      : make_uint2(kv4_pair<BF16, 0>(two, sc), kv4_pair<BF16, 1>(two, sc));
+        }
+      }
+    }
+  };
+  // Clear the V rows of this wave's page of step s that no query of the tile
+  // sees: they may hold anything, and 0 * NaN is not 0.  After the page has
+  // landed, before the others read it.
+  auto clear_unseen = [&](int id, int s, Tile& vt) __attribute__((always_inline)) {
+    const int b0 = base_of(s);
+    const bool all = id < 0 || (b0 + 15 <= p_last &&
+                                (p_first - b0 < window || b0 + 15 < a.sinks));
+    if (all) return;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int t = b0 + KPL * i + lk;
+      if (t > p_last || (p_first - t >= window && t >= a.sinks))
+        vt[16 * wave + KPL * i + lk][lc] = zero4();
     }
   };
 
+  // This wave's loads have reached LDS.
+  auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+
+  // The running maximum is kept this far (log2) below the largest score: an f16
+  // weight of up to 2^15 then stays normal down to 2^-21 of the largest.
+  constexpr float kRoom = BF16 ? 0.f : 7.f;
+
+  // ---- one step ---------------------------------------------------------------------
   float m_run = kLowest, l_part = 0.f;
   f32x16 acc[NC];
 #pragma unroll
@@ -260,42 +268,42 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[cb][i] = 0.f;
 
-  auto compute = [&](int buf, const Pages& pg) {
-    bool full = true, any = false;
+  auto scores = [&](const Tile& kt, f32x16 (&s)[2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int b0 = pg.base[x];
-      full &= b0 + 15 <= pw_first && (a.window == 0 || b0 > pw_last - a.window ||
-                                      b0 + 15 < a.sinks);
-      any |= b0 <= pw_last && (a.window == 0 || b0 + 15 > pw_first - a.window || b0 < a.sinks);
-    }
-    if (!any || !busy) return;
-    f32x16 s[2];
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+    for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[sub][i] = 0.f;
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) {
+    for (int t = 0; t < NQ; ++t)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
         const int key = 32 * sub + n;
-        s[sub] = mfma32<BF16>(sh.k[buf][key][k_chunk<D>(key, 2 * t + h)], qf[t], s[sub]);
+        s[sub] = mfma32<BF16>(kt[key][k_chunk<D>(key, 2 * t + h)], qf[t], s[sub]);
       }
-    }
-    if (!full) {
+  };
+  // `bad`: this step has absent pages (a bit each).
+  auto mask = [&](int st, uint32_t bad, f32x16 (&s)[2]) {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
+    for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = pg.base[2 * sub + (i >> 3)] + 8 * ((i >> 2) & 1) + 4 * h + (i & 3);
-          if (!sees(p, t, a.window, a.sinks)) s[sub][i] = kNegInf;
-        }
-    }
+      for (int i = 0; i < 16; ++i) {
+        const int x = 2 * sub + (i >> 3), v = 4 * st + x;
+        const int b0 = ((bad >> x) & 1) ? kNoPage : 16 * (v < sp.ahead ? v : v + sp.skip);
+        const int t = b0 + 8 * ((i >> 2) & 1) + 4 * h + (i & 3);
+        // t > p wraps to a large unsigned number
+        const bool ok = (static_cast<uint32_t>(p - t) < static_cast<uint32_t>(window)) |
+                        (t < min(a.sinks, p + 1));
+        if (!ok) s[sub][i] = kNegInf;
+      }
+  };
+  const int kq = (lane & 15) >> 2, cq = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  auto softmax_pv = [&](const Tile& vt, const f32x16 (&s)[2]) __attribute__((always_inline)) {
     float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
     top = max_x32(top) * a.scale_log2;
-    if (__builtin_amdgcn_ballot_w64(top > m_run + kSlack) != 0) {
-      const float mn = fmaxf(m_run, top);
+    if (__builtin_amdgcn_ballot_w64(top > m_run + kRoom + kSlack) != 0) {
+      const float mn = fmaxf(m_run, top - kRoom);
       const float alpha = fast_exp2(m_run - mn);
       l_part *= alpha;
 #pragma unroll
@@ -311,12 +319,11 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
       for (int i = 0; i < 8; ++i) {
         const float e0 = fast_exp2(fmaf(s[sub][2 * i], a.scale_log2, -m_run));
         const float e1 = fast_exp2(fmaf(s[sub][2 * i + 1], a.scale_log2, -m_run));
-        l_part += e0 + e1;
         pb[sub][i] = pack2<BF16>(e0, e1);
+        l_part += e0 + e1;
       }
     // Lane's share of a transposed read: key lane % 16 / 4 of four, 16-byte
     // chunk 2 (lane / 16 % 2) + lane % 4 / 2 of a channel block, half lane % 2.
-    const int kq = (lane & 15) >> 2, cq = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const uint4 bv = make_uint4(pb[ks >> 1][4 * (ks & 1)], pb[ks >> 1][4 * (ks & 1) + 1],
@@ -324,35 +331,117 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
 #pragma unroll
       for (int cb = 0; cb < NC; ++cb) {
         const int key = 16 * ks + 4 * h + kq;
-        const uint2* p0 =
-            reinterpret_cast<const uint2*>(&sh.v[buf][key][v_chunk<D>(key, 4 * cb + cq)]) +
-            (lane & 1);
-        const uint2* p1 =
-            reinterpret_cast<const uint2*>(&sh.v[buf][key + 8][v_chunk<D>(key + 8, 4 * cb + cq)]) +
-            (lane & 1);
-        const uint2 v0 = read_transposed(p0), v1 = read_transposed(p1);
+        const uint2 v0 = read_transposed(
+            reinterpret_cast<const uint2*>(&vt[key][v_chunk<D>(key, 4 * cb + cq)]) +
+            (lane & 1));
+        const uint2 v1 = read_transposed(
+            reinterpret_cast<const uint2*>(&vt[key + 8][v_chunk<D>(key + 8, 4 * cb + cq)]) +
+            (lane & 1));
         acc[cb] = mfma32<BF16>(make_uint4(v0.x, v0.y, v1.x, v1.y), bv, acc[cb]);
       }
     }
   };
 
-  issue(0);
-  put(0);
-  Pages cur = next;
-  if (steps > 1) issue(1);
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    compute(s & 1, cur);
-    if (s + 1 < steps) {
-      put((s + 1) & 1);
-      cur = next;
-      if (s + 2 < steps) issue(s + 2);
+  // ---- the walk -----------------------------------------------------------------------
+  // During step s, K of step s + 2 and V of step s + 1 are under way.
+  int ids0 = s_begin, ids = load_ids(s_begin), ids_next = load_ids(s_begin + 16);
+  uint64_t no_page = __builtin_amdgcn_ballot_w64(ids < 0);
+  // This wave's page of a step, and the step's absent pages (a bit each).
+  struct StepPages {
+    int id;
+    uint32_t bad;
+  };
+  auto pages_of = [&](int s) {
+    StepPages r{-1, 15u};
+    if (s >= s_end) return r;
+    if (s - ids0 >= 16) {
+      ids0 += 16;
+      ids = ids_next;
+      ids_next = load_ids(ids0 + 16);
+      no_page = __builtin_amdgcn_ballot_w64(ids < 0);
     }
+    const int at = 4 * (s - ids0);
+    r.id = __builtin_amdgcn_readlane(ids, at + wave);
+    r.bad = static_cast<uint32_t>(no_page >> at) & 15u;
+    return r;
+  };
+  StepPages pg0 = pages_of(s_begin), pg1 = pages_of(s_begin + 1);
+  issue_k(pg0.id, s_begin, kt0);
+  issue_v(pg0.id, s_begin, vt0);
+  put_k(kt0);
+  issue_k(pg1.id, s_begin + 1, kt1);
+  put_k(kt1);
+  put_v(vt0);
+  landed();
+  clear_unseen(pg0.id, s_begin, vt0);
+  __syncthreads();
+  f32x16 sa[2], sb[2];
+  scores(kt0, sa);
+  __syncthreads();  // kt0 is free
+  // One step: `sc` holds its scores, `sn` gets the next step's (of nothing
+  // behind the last: not used).
+  auto step = [&](int s, Tile& k_cur, Tile& k_next, Tile& v_cur, Tile& v_next, f32x16 (&sc)[2],
+                  f32x16 (&sn)[2]) __attribute__((always_inline)) {
+    const StepPages pg2 = pages_of(s + 2);
+    issue_k(pg2.id, s + 2, k_cur);
+    issue_v(pg1.id, s + 1, v_next);
+    scores(k_next, sn);
+    const bool full = (s >= full_lo && s < full_hi) || s < sink_hi;
+    if (!full || pg0.bad) mask(s, pg0.bad, sc);
+    softmax_pv(v_cur, sc);
+    put_k(k_cur);
+    put_v(v_next);
+    landed();
+    clear_unseen(pg1.id, s + 1, v_next);
+    pg0 = pg1, pg1 = pg2;
     __syncthreads();
+  };
+  for (int s = s_begin; s < s_end; s += 2) {
+    step(s, kt0, kt1, vt0, vt1, sa, sb);
+    if (s + 1 < s_end) step(s + 1, kt1, kt0, vt1, vt0, sb, sa);
   }
 
   // ---- outputs ----------------------------------------------------------------
-  const float l = sum_x32(l_part);
+  float l = sum_x32(l_part);
+  const int ns = (all_steps + per_split - 1) / per_split;
+  if (ns > 1) {
+    // State of a split: [d / 2 pairs][thread][2] of O and [thread][2] of m, l.
+    const int64_t tg = int64_t(item) * a.num_kv_heads + g;
+    constexpr int64_t kSlot = 256 * (D / 2 + 2);
+    float* mine_st = a.state + (tg * a.splits + split) * kSlot;
+#pragma unroll
+    for (int cb = 0; cb < NC; ++cb)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        put_state(mine_st + ((cb * 8 + i) * 256 + tid) * 2, acc[cb][2 * i], acc[cb][2 * i + 1]);
+    put_state(mine_st + (NC * 8 * 256 + tid) * 2, m_run, l);
+    if (!last_to_arrive(a.arrivals + tg, ns, &s_last)) return;
+    // Joined in split order, so that the result does not depend on the order
+    // of arrival: first the maximum, then the weighted sums.
+    const float* st0 = a.state + tg * a.splits * kSlot;
+    m_run = kLowest;
+    for (int s = 0; s < ns; ++s)
+      m_run = fmaxf(m_run, get_state2(st0 + s * kSlot + (NC * 8 * 256 + tid) * 2).x);
+    l = 0.f;
+#pragma unroll
+    for (int cb = 0; cb < NC; ++cb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[cb][i] = 0.f;
+    for (int s = 0; s < ns; ++s) {
+      const float* st = st0 + s * kSlot;
+      const float2 ml = get_state2(st + (NC * 8 * 256 + tid) * 2);
+      const float w = fast_exp2(ml.x - m_run);
+      l = fmaf(w, ml.y, l);
+#pragma unroll
+      for (int cb = 0; cb < NC; ++cb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 o = get_state2(st + ((cb * 8 + i) * 256 + tid) * 2);
+          acc[cb][2 * i] = fmaf(w, o.x, acc[cb][2 * i]);
+          acc[cb][2 * i + 1] = fmaf(w, o.y, acc[cb][2 * i + 1]);
+        }
+    }
+  }
   if (!mine) return;
   const bool none = l == 0.f;
   const float inv = none ? 0.f : 1.f / l;
@@ -380,7 +469,7 @@ void launch_fmt(bool kv4, const PromptArgs& a, int tiles, uint32_t grid, hipStre
 pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hipStream_t s) {
   const int64_t tiles = prompt_tiles(a);
   const bool bf = p.dtype == PKV_BF16;
-  const uint32_t n = static_cast<uint32_t>(tiles * a.num_kv_heads);
+  const uint32_t n = static_cast<uint32_t>(tiles * a.num_kv_heads * a.splits);
   if (p.head_dim == 128) {
     if (bf) launch_fmt<128, true>(kv4, a, static_cast<int>(tiles), n, s);
     else launch_fmt<128, false>(kv4, a, static_cast<int>(tiles), n, s);

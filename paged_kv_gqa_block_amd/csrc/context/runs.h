@@ -47,6 +47,9 @@ __device__ __forceinline__ Run run_of(const int32_t* tok_offsets, const int32_t*
     r.count = 1;
   }
   r.len = clean_len(seq_lens[row], max_pages);
+  r.first = __builtin_amdgcn_readfirstlane(r.first);
+  r.count = __builtin_amdgcn_readfirstlane(r.count);
+  r.len = __builtin_amdgcn_readfirstlane(r.len);
   return r;
 }
 

@@ -363,23 +363,34 @@ class Kv4Step(WindowStep):
 
 class PromptStep(_ContextCalls):
     """Causal attention of up to `num_tokens` new tokens, all rows together,
-    over a 16-bit or 4-bit cache that already holds them.
+    over a 16-bit or 4-bit cache that already holds them.  Owns the output and
+    the workspace, as ``WindowStep``.
 
     ``run`` takes q [num_tokens][Hq][d], tok_offsets [B + 1] (or None for one
     token per row), block_table, seq_lens and k_pool, v_pool or kv4_pool.
     """
 
     def __init__(self, prob: _lib.pkv_problem, num_tokens: int, window: int = 0, sinks: int = 0,
-                 device="cuda"):
+                 splits: int | None = None, device="cuda"):
         super().__init__(prob, device)
         self.view = _context.make_view(window, sinks)
         self.num_tokens = num_tokens
+        if splits is None:
+            splits = _context.pkv_prompt_splits(
+                prob, self.view, num_tokens, False, torch.cuda.get_device_properties(
+                    self.device).multi_processor_count)
+        self.splits = splits
+        nbytes = _context.pkv_prompt_workspace_bytes(prob, num_tokens, False, splits)
+        if num_tokens == prob.batch:  # room for calls without tok_offsets too
+            nbytes = max(nbytes, _context.pkv_prompt_workspace_bytes(prob, num_tokens, True,
+                                                                     splits))
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
                                device=self.device)
         self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
                                device=self.device)
         self._view_ref = ctypes.byref(self.view)
-        self._own = (self.out.data_ptr(), self.lse.data_ptr())
+        self._own = (self.workspace.data_ptr(), nbytes, self.out.data_ptr(), self.lse.data_ptr())
 
     def bind(self, w: dict, stream=None) -> tuple:
         n = self.num_tokens
@@ -387,7 +398,8 @@ class PromptStep(_ContextCalls):
         table, lens = self._tables(w["block_table"], w["seq_lens"])
         pools = self._pools(w)
         return ("pkv_prompt_kv4" if len(pools) == 1 else "pkv_prompt_window", self._view_ref,
-                self._offsets(w.get("tok_offsets"), n), n, lens, q, *pools, table, *self._own,
+                self._offsets(w.get("tok_offsets"), n), n, lens, self.splits, q, *pools, table,
+                *self._own,
                 self._stream(stream))
 
     def run(self, w: dict, stream=None) -> tuple:

@@ -58,6 +58,22 @@ def test_workspace_and_splits():
     assert _context.pkv_attend_splits(_prob(), _context.make_view(-1, 0), 256) == 0
 
 
+def test_prompt_workspace_and_splits():
+    ws, sp = _context.pkv_prompt_workspace_bytes, _context.pkv_prompt_splits
+    p = _prob(max_pages_per_row=2048)
+    tiles = 10 * 4 // 128 + 2
+    assert ws(p, 10, False, 1) == 0
+    assert ws(p, 10, False, 3) >= tiles * 2 * 3 * 128 * (128 + 2) * 4
+    assert ws(p, 2, True, 3) >= 2 * 2 * 3 * 128 * (128 + 2) * 4
+    assert ws(p, 3, True, 3) == 0 and ws(p, -1, False, 3) == 0 and ws(p, 10, False, 0) == 0
+    assert ws(p, 2 ** 31 - 1, False, 2) == 0
+    s = [sp(p, None, n, False, 256) for n in (1, 100, 10000, 100000)]
+    assert s == sorted(s, reverse=True) and s[0] > 1 and s[-1] == 1
+    assert sp(p, _context.make_view(16, 0), 10, False, 256) == 1
+    assert sp(p, None, 0, False, 256) >= 1 and sp(p, None, 10, False, 0) == 0
+    assert sp(p, _context.make_view(-1, 0), 10, False, 256) == 0 and sp(p, None, 3, True, 256) == 0
+
+
 def _attend(kv4=False, prob=None, view=None, lens=P, splits=4, q=P, k=P, v=P, bt=P, ws=P,
             ws_bytes=1 << 30, out=P, lse=None):
     prob = prob or _prob()
@@ -95,13 +111,14 @@ def test_attend_refusals(kv4):
     assert _attend(kv4, prob=_prob(batch=0)) == PKV_EINVAL
 
 
-def _prompt(kv4=False, prob=None, view=None, off=P, n=10, lens=P, q=P, k=P, v=P, bt=P, out=P):
+def _prompt(kv4=False, prob=None, view=None, off=P, n=10, lens=P, splits=1, q=P, k=P, v=P, bt=P,
+            ws=None, ws_bytes=0, out=P):
     prob = prob or _prob()
     view = None if view is None else ctypes.byref(_context.make_view(*view))
-    head = (ctypes.byref(prob), view, off, n, lens, q)
+    head, tail = (ctypes.byref(prob), view, off, n, lens, splits, q), (ws, ws_bytes, out, None, None)
     if kv4:
-        return _lib.LIB.pkv_prompt_kv4(*head, k, bt, out, None, None)
-    return _lib.LIB.pkv_prompt_window(*head, k, v, bt, out, None, None)
+        return _lib.LIB.pkv_prompt_kv4(*head, k, bt, *tail)
+    return _lib.LIB.pkv_prompt_window(*head, k, v, bt, *tail)
 
 
 @pytest.mark.parametrize("kv4", [False, True])
@@ -115,6 +132,13 @@ def test_prompt_refusals(kv4):
     for name in ("q", "k", "out"):
         assert _prompt(kv4, **{name: P + 2}) == PKV_ESHAPE, name
     assert _prompt(kv4, n=2 ** 31 - 1) == PKV_ERANGE
+    for s in (0, -1, 65536):
+        assert _prompt(kv4, splits=s) == PKV_EINVAL
+    assert _prompt(kv4, splits=2) == PKV_EINVAL  # needs a workspace
+    assert _prompt(kv4, splits=2, ws=P + 8, ws_bytes=1 << 30) == PKV_ESHAPE
+    need = _context.pkv_prompt_workspace_bytes(_prob(), 10, False, 2)
+    assert need > 0 and _prompt(kv4, splits=2, ws=P, ws_bytes=need - 1) == PKV_ENOSPC
+    assert _prompt(kv4, splits=65535, n=8000, ws=P, ws_bytes=1 << 60) == PKV_ERANGE
     assert _prompt(kv4, n=0) == PKV_OK
     assert _prompt(kv4, n=0, prob=_prob(head_dim=80)) == PKV_ESHAPE
 
