@@ -59,10 +59,12 @@ def pkv_kv4_page_bytes(head_dim: int) -> int:
 
 def token_stride(x) -> int:
     """Elements between the tokens of [tokens][Hkv][d] with contiguous heads."""
-    if x.dim() != 3 or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+    n, heads, d = x.shape
+    token, head, one = x.stride()
+    if one != 1 or (head != d and heads > 1):
         raise ValueError("new keys and values are [tokens][Hkv][d] with contiguous heads")
     # A single token's stride carries no meaning.
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return token if n > 1 else heads * d
 
 
 def pkv_store_kv(prob, tok_offsets, num_tokens: int, seq_lens_dev, k_new, v_new, block_table,

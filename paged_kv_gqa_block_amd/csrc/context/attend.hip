@@ -452,16 +452,17 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3,8))) 
   }
 }
 
+template <int D, bool BF16, bool KV4, int GP>
+void launch_one(const AttendArgs& a, hipStream_t s) {
+  const dim3 grid(a.num_kv_heads, a.splits, a.batch);
+  hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, GP, 4, KV4 ? 2 : 1>), grid, dim3(256), 0, s, a);
+}
+
 template <int D, bool BF16, bool KV4>
 void launch_gp(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid(a.num_kv_heads, a.splits, a.batch);
-  constexpr int PF = KV4 ? 2 : 1;
-  if (a.group <= 4)
-    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 4, 4, PF>), grid, dim3(256), 0, s, a);
-  else if (a.group <= 8)
-    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 8, 4, PF>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((attend_kernel<D, BF16, KV4, 16, 4, PF>), grid, dim3(256), 0, s, a);
+  if (a.group <= 4) launch_one<D, BF16, KV4, 4>(a, s);
+  else if (a.group <= 8) launch_one<D, BF16, KV4, 8>(a, s);
+  else launch_one<D, BF16, KV4, 16>(a, s);
 }
 
 template <int D, bool BF16>

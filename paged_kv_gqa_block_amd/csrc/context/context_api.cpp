@@ -280,12 +280,12 @@ extern "C" int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* vi
   const int64_t pairs = int64_t(prob->batch) * prob->num_kv_heads;
   const int64_t pages = most_pages(prob, view);
   // One range for every compute unit, as long as a range keeps eight pages (one
-  // unit for each wave); beyond that ranges of at least 128 pages, up to twelve
+  // unit for each wave); beyond that ranges of at least 96 pages, up to twelve
   // a compute unit, so that rows of different lengths even out.  Joining costs
   // more than it gives where ranges are shorter: 64 pairs of 2048 pages took
   // 51 us in 4, 34 us in 16 and 38 us in 32 ranges each.
   const int64_t fill = std::min(ceil_div(num_cus, pairs), ceil_div(pages, 8));
-  const int64_t even = std::min(pages / 128, int64_t(12) * num_cus / pairs);
+  const int64_t even = std::min(pages / 96, int64_t(12) * num_cus / pairs);
   return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::max(fill, even), 1024)));
 }
 

@@ -78,6 +78,14 @@ __device__ __forceinline__ float sum_x32(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Largest of three, one instruction: fmaxf of matrix-core results would first
+// quieten each operand.  A NaN loses against a number, as with fmaxf.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // Where a running maximum starts: finite, so that a score of -inf weighs
 // exp2(-inf) = 0 and never meets -inf - -inf.
 constexpr float kLowest = -3.402823466e38f;

@@ -89,13 +89,14 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const int item = tiles - 1 - ts / a.splits;
   const int G = a.group;
 
-  int row = item, k_tile = 0;
+  int k_tile = 0;
+  Run run;
   if (a.tok_offsets) {
-    row = find_row(a.tok_offsets, a.batch, a.num_tokens, item,
-                   [&](int64_t off, int64_t r) { return tile_base(off, r, G); });
+    run = find_run(a, item, [&](int64_t off, int64_t r) { return tile_base(off, r, G); });
+    k_tile = item - static_cast<int>(tile_base(run.first, run.row, G));
+  } else {
+    run = single_run(a, item);
   }
-  const Run run = run_of(a.tok_offsets, a.seq_lens, row, a.num_tokens, a.max_pages);
-  if (a.tok_offsets) k_tile = item - static_cast<int>(tile_base(run.first, row, G));
   const int64_t rows64 = int64_t(run.count) * G;
   if (k_tile < 0 || int64_t(k_tile) * kTileRows >= rows64) return;
   const int r0 = k_tile * kTileRows;
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const int per_split = (all_steps + a.splits - 1) / a.splits;
   const int s_begin = split * per_split, s_end = min(s_begin + per_split, all_steps);
   if (s_begin >= s_end) return;
-  const int32_t* bt = a.block_table + int64_t(row) * a.max_pages;
+  const int32_t* bt = a.block_table + int64_t(run.row) * a.max_pages;
 
   // B operand of the scores: channels 16 t + 8 h .. of this lane's query.
   uint4 qf[NQ];
@@ -298,10 +299,13 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   };
   const int kq = (lane & 15) >> 2, cq = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   auto softmax_pv = [&](const Tile& vt, const f32x16 (&s)[2]) __attribute__((always_inline)) {
-    float top = fmaxf(s[0][0], s[1][0]);
+    float t0 = max3(s[0][0], s[1][0], s[1][0]), t1 = max3(s[0][1], s[1][1], s[1][1]);
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
-    top = max_x32(top) * a.scale_log2;
+    for (int i = 2; i < 16; i += 2) {
+      t0 = max3(t0, s[0][i], s[1][i]);
+      t1 = max3(t1, s[0][i + 1], s[1][i + 1]);
+    }
+    const float top = max_x32(fmaxf(t0, t1)) * a.scale_log2;
     if (__builtin_amdgcn_ballot_w64(top > m_run + kRoom + kSlack) != 0) {
       const float mn = fmaxf(m_run, top - kRoom);
       const float alpha = fast_exp2(m_run - mn);
@@ -419,9 +423,18 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
     // Joined in split order, so that the result does not depend on the order
     // of arrival: first the maximum, then the weighted sums.
     const float* st0 = a.state + tg * a.splits * kSlot;
+    constexpr int U = 8;  // splits whose m and l are under way together
+    auto get_ml = [&](int s) {
+      return get_state2(st0 + min(s, ns - 1) * kSlot + (NC * 8 * 256 + tid) * 2);
+    };
     m_run = kLowest;
-    for (int s = 0; s < ns; ++s)
-      m_run = fmaxf(m_run, get_state2(st0 + s * kSlot + (NC * 8 * 256 + tid) * 2).x);
+    for (int s0 = 0; s0 < ns; s0 += U) {
+      float2 ml[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) ml[u] = get_ml(s0 + u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) m_run = fmaxf(m_run, ml[u].x);
+    }
     l = 0.f;
 #pragma unroll
     for (int cb = 0; cb < NC; ++cb)
@@ -429,7 +442,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
       for (int i = 0; i < 16; ++i) acc[cb][i] = 0.f;
     for (int s = 0; s < ns; ++s) {
       const float* st = st0 + s * kSlot;
-      const float2 ml = get_state2(st + (NC * 8 * 256 + tid) * 2);
+      const float2 ml = get_ml(s);
       const float w = fast_exp2(ml.x - m_run);
       l = fmaf(w, ml.y, l);
 #pragma unroll

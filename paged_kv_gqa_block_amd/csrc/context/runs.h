@@ -18,39 +18,45 @@ __device__ __forceinline__ int clamp_offset(int off, int num_tokens) {
   return min(max(off, 0), num_tokens);
 }
 
-// The last row i with base(off_i, i) <= item, where base grows with i: every
-// wave counts the rows below by itself, 64 at a time.
-template <typename Base>
-__device__ __forceinline__ int find_row(const int32_t* tok_offsets, int batch, int num_tokens,
-                                        int64_t item, Base base) {
-  const int lane = threadIdx.x & 63;
-  int below = 0;
-  for (int r0 = 0; r0 < batch; r0 += 64) {
-    const int r = r0 + lane;
-    const bool in = r < batch && base(clamp_offset(tok_offsets[r], num_tokens), r) <= item;
-    const int k = __popcll(__builtin_amdgcn_ballot_w64(in));
-    below += k;
-    if (k < 64) break;
-  }
-  return max(__builtin_amdgcn_readfirstlane(below) - 1, 0);
-}
-
-__device__ __forceinline__ Run run_of(const int32_t* tok_offsets, const int32_t* seq_lens, int row,
-                                      int num_tokens, int max_pages) {
+__device__ __forceinline__ Run make_run(int row, int first, int next, int len, int max_pages) {
   Run r;
   r.row = row;
-  if (tok_offsets) {
-    r.first = clamp_offset(tok_offsets[row], num_tokens);
-    r.count = max(clamp_offset(tok_offsets[row + 1], num_tokens) - r.first, 0);
-  } else {
-    r.first = row;
-    r.count = 1;
-  }
-  r.len = clean_len(seq_lens[row], max_pages);
-  r.first = __builtin_amdgcn_readfirstlane(r.first);
-  r.count = __builtin_amdgcn_readfirstlane(r.count);
-  r.len = __builtin_amdgcn_readfirstlane(r.len);
+  r.first = __builtin_amdgcn_readfirstlane(first);
+  r.count = max(__builtin_amdgcn_readfirstlane(next) - r.first, 0);
+  r.len = clean_len(__builtin_amdgcn_readfirstlane(len), max_pages);
   return r;
+}
+
+// The run of work item `item`: that of the last row i with base(off_i, i) <=
+// item, where base grows with i.  Every wave finds it by itself, 64 rows at a
+// time; offsets and lengths of the first 64 come with one round of loads.
+template <typename Args, typename Base>
+__device__ __forceinline__ Run find_run(const Args& a, int64_t item, Base base) {
+  const int lane = threadIdx.x & 63;
+  int below = 0, off = 0, len = 0, r0 = 0;
+  for (;; r0 += 64) {
+    const int r = r0 + lane;
+    off = r <= a.batch ? clamp_offset(a.tok_offsets[r], a.num_tokens) : a.num_tokens;
+    len = r < a.batch ? a.seq_lens[r] : 0;
+    const bool in = r < a.batch && base(off, r) <= item;
+    const int k = __popcll(__builtin_amdgcn_ballot_w64(in));
+    below += k;
+    if (k < 64 || r0 + 64 >= a.batch) break;
+  }
+  const int row = max(__builtin_amdgcn_readfirstlane(below) - 1, 0);
+  const int at = row - r0;  // 0 .. 62: the row and its successor are in hand
+  if (at >= 0 && at < 63)
+    return make_run(row, __builtin_amdgcn_readlane(off, at), __builtin_amdgcn_readlane(off, at + 1),
+                    __builtin_amdgcn_readlane(len, at), a.max_pages);
+  return make_run(row, clamp_offset(a.tok_offsets[row], a.num_tokens),
+                  clamp_offset(a.tok_offsets[row + 1], a.num_tokens), a.seq_lens[row],
+                  a.max_pages);
+}
+
+// The one new token of a row, without offsets.
+template <typename Args>
+__device__ __forceinline__ Run single_run(const Args& a, int row) {
+  return make_run(row, row, row + 1, a.seq_lens[row], a.max_pages);
 }
 
 // A page's share of a run: tokens [begin, end) of block-table entry `entry`
@@ -67,12 +73,10 @@ __device__ __forceinline__ Segment find_segment(const Args& a, int item) {
   Segment s;
   int k = 0;
   if (a.tok_offsets) {
-    const int row = find_row(a.tok_offsets, a.batch, a.num_tokens, item,
-                             [](int64_t off, int64_t r) { return segment_base(off, r); });
-    s.run = run_of(a.tok_offsets, a.seq_lens, row, a.num_tokens, a.max_pages);
-    k = item - static_cast<int>(segment_base(s.run.first, row));
+    s.run = find_run(a, item, [](int64_t off, int64_t r) { return segment_base(off, r); });
+    k = item - static_cast<int>(segment_base(s.run.first, s.run.row));
   } else {
-    s.run = run_of(nullptr, a.seq_lens, item, a.num_tokens, a.max_pages);
+    s.run = single_run(a, item);
   }
   const int p0 = max(s.run.len - s.run.count, 0);  // negative positions are not in the cache
   s.entry = (p0 >> 4) + k;

@@ -195,6 +195,7 @@ class _ContextCalls:
                         "tok_offsets": (p.batch + 1,),
                         "kv4_pool": (p.num_pool_pages, p.num_kv_heads, self.kv4_page_bytes),
                         "pool": (p.num_pool_pages, p.num_kv_heads, p.page_size, p.head_dim),
+                        "token": (p.num_kv_heads, p.head_dim),
                         "q": (p.batch, p.num_q_heads, p.head_dim)}
         self._prob_ref = ctypes.byref(prob)
 
@@ -238,8 +239,7 @@ class _ContextCalls:
 
     def _new_tokens(self, name: str, t: torch.Tensor, n: int) -> tuple:
         """Address and token stride of new keys or values."""
-        p = self.prob
-        if t.shape != (n, p.num_kv_heads, p.head_dim) or t.dtype != self.dtype or \
+        if t.shape != (n, *self._shapes["token"]) or t.dtype != self.dtype or \
                 t.device != self.device:
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
         return t.data_ptr(), _context.token_stride(t)
@@ -284,8 +284,8 @@ class Kv4Cache(_ContextCalls):
 
     def load(self, block_table, seq_lens, tok_offsets, k_out, v_out, stream=None) -> tuple:
         """The values the cache stands for, into k_out, v_out [tokens][Hkv][d]."""
-        p, n = self.prob, k_out.shape[0]
-        shape = (n, p.num_kv_heads, p.head_dim)
+        n = k_out.shape[0]
+        shape = (n, *self._shapes["token"])
         table, lens = self._tables(block_table, seq_lens)
         self._launch("pkv_kv4_load", self._offsets(tok_offsets, n), n, lens, table,
                      self.pool.data_ptr(), self._expect("k_out", k_out, shape, self.dtype),
