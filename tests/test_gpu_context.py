@@ -501,3 +501,165 @@ def test_refusals_on_the_device():
                                           device="cuda").as_strided((2, 2, 128), (260, 128, 1)),
                         torch.zeros(2, 2, 128, dtype=torch.float16, device="cuda"),
                         w["block_table"], w["seq_lens"], None, w["k_pool"], w["v_pool"])
+
+
+# ---- larger sizes, shared buffers -----------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [63, 64, 65, 130])
+def test_runs_of_many_rows(rows):
+    """Rows around and beyond what a wave holds, some without new tokens: the
+    prompt, the store and the read-back find every token's row."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, 40, rows)
+    new = np.minimum(lens, rng.integers(0, 20, rows))
+    new[rng.random(rows) < 0.3] = 0
+    say(f"[many runs] rows={rows} tokens={new.sum()}")
+    b = Batch(rows, lens, new, hkv=1, group=3, d=64, window=15, sinks=2, kv4=True)
+    w = b.device()
+    n = int(new.sum())
+    out, lse = engine.PromptStep(b.problem(), n, 15, 2).run(w)
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "f16", 64, b.vmax, True, "many runs")
+    cache = engine.Kv4Cache(b.problem())
+    x = torch.from_numpy(rng.standard_normal((n, 1, 64), dtype=np.float32)).half().cuda()
+    cache.store(x, -x, w["block_table"], w["seq_lens"], w["tok_offsets"])
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    cache.load(w["block_table"], w["seq_lens"], w["tok_offsets"], k, v)
+    torch.cuda.synchronize()
+    want = oc.kv4_values(*oc.kv4_quantise(f64(x), "f16"))
+    np.testing.assert_array_equal(f64(k), want)
+    np.testing.assert_array_equal(f64(v), -want)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_pages_beyond_4_gib(kv4):
+    """The same rows in a small pool and at the far end of a pool whose byte
+    offsets pass 2^32: every call gives the same bits."""
+    b = Batch(21, [300, 77], [40, 77], hkv=8, group=2, window=100, sinks=3, kv4=kv4, dtype="bf16")
+    w = b.device()
+    small = (w["kv4_pool"] if kv4 else w["k_pool"]).shape[0]
+    page_bytes = 8 * (17 * 128 if kv4 else 16 * 128 * 2)
+    big = (1 << 32) // page_bytes + 1000
+    shift = big - small
+    prob = b.problem(num_pool_pages=big)
+    far = dict(w, block_table=w["block_table"] + shift)
+    say(f"[far pages] kv4={kv4} pages={big}")
+    for name in ("kv4_pool",) if kv4 else ("k_pool", "v_pool"):
+        far[name] = torch.zeros(big, *w[name].shape[1:], dtype=w[name].dtype, device="cuda")
+        far[name][shift:] = w[name]
+    n = int(b.new.sum())
+    qd = {"q": w["q"][:2].contiguous()}
+    outs = []
+    for pr, x in ((b.problem(), w), (prob, far)):
+        got = [t.clone() for t in engine.PromptStep(pr, n, 100, 3).run(x)]
+        cls = engine.Kv4Step if kv4 else engine.WindowStep
+        got += [t.clone() for t in cls(pr, 100, 3).run(dict(x, **qd))]
+        kv = torch.linspace(-3, 3, n * 8 * 128, device="cuda").to(torch.bfloat16).view(n, 8, 128)
+        args = (x["block_table"], x["seq_lens"], x["tok_offsets"])
+        if kv4:
+            cache = engine.Kv4Cache(pr, pool=x["kv4_pool"])
+            cache.store(kv, kv, *args)
+            got += list(cache.load(*args, torch.empty_like(kv), torch.empty_like(kv)))
+            got.append(x["kv4_pool"][-small:].clone())
+        else:
+            engine.store_kv(pr, kv, kv, *args, x["k_pool"], x["v_pool"])
+            got += [x["k_pool"][-small:].clone(), x["v_pool"][-small:].clone()]
+        torch.cuda.synchronize()
+        outs.append(got)
+    for a, c in zip(*outs):
+        assert _same(a, c)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40])
+def test_prompt_splits(splits):
+    """Few queries over long contexts, the keys cut into ranges; twice on one
+    workspace, with the same bits."""
+    for kv4, d, dtype in ((False, 128, "bf16"), (False, 64, "f16"), (True, 128, "f16")):
+        say(f"[prompt splits] {splits} kv4={kv4} d={d} {dtype}")
+        b = Batch(splits, [1500, 0, 70, 900], [3, 0, 70, 33], hkv=2, group=4, d=d, dtype=dtype,
+                  kv4=kv4, window=1200, sinks=20)
+        step = engine.PromptStep(b.problem(), int(b.new.sum()), 1200, 20, splits)
+        w = b.device()
+        out, lse = step.run(w)
+        torch.cuda.synchronize()
+        check(out, lse, b.reference(), dtype, d, b.vmax, True, f"splits {splits}")
+        first = out.clone(), lse.clone()
+        step.run(w)
+        torch.cuda.synchronize()
+        assert _same(first[0], step.out) and _same(first[1], step.lse)
+
+
+def test_two_graphs_of_one_step_replayed_in_turn():
+    """Two captured graphs that share a step's workspace, one after the other."""
+    b = Batch(17, [900, 450], hkv=2, group=4, window=0)
+    step, w = _step(b, 16), b.device()
+    other = dict(w, q=torch.randn_like(w["q"]))
+    outs = [step.run(x)[0].clone() for x in (w, other)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step.run(w)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for x in (w, other):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step.run(x)
+        graphs.append(g)
+    for i in range(6):
+        say(f"[two graphs] replay {i}")
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert _same(step.out, outs[i % 2])
+
+
+def test_bound_calls_follow_their_buffers():
+    b = Batch(18, [200, 33], window=50, sinks=2)
+    step, w = _step(b), b.device()
+    bound = step.bind(w)
+    first = step.run_bound(bound)[0].clone()
+    w["q"].mul_(-1)
+    second = step.run_bound(bound)[0].clone()
+    w["q"].mul_(-1)
+    third = step.run_bound(bound)[0].clone()
+    torch.cuda.synchronize()
+    assert _same(first, third) and not _same(first, second)
+
+
+def test_no_new_tokens_at_all():
+    b = Batch(19, [20, 5], [0, 0], kv4=True)
+    w, prob = b.device(), b.problem()
+    empty = torch.empty(0, 2, 128, dtype=torch.float16, device="cuda")
+    cache = engine.Kv4Cache(prob, pool=w["kv4_pool"])
+    before = cache.pool.clone()
+    args = (w["block_table"], w["seq_lens"], w["tok_offsets"])
+    cache.store(empty, empty, *args)
+    cache.load(*args, empty, empty.clone())
+    out, lse = engine.PromptStep(prob, 0).run(dict(w, q=w["q"]))
+    torch.cuda.synchronize()
+    assert _same(before, cache.pool) and out.numel() == 0 and lse.numel() == 0
+
+
+def test_unordered_offsets_stay_in_bounds():
+    """Offsets that break the contract (decreasing, negative, beyond the token
+    count) give rows that nobody promised, but touch nothing outside the
+    buffers: guard rows around them keep their values."""
+    b = Batch(20, [40, 40, 40, 40], [10, 10, 10, 10], kv4=True)
+    w, prob = b.device(), b.problem()
+    n = 40
+    out = torch.full((n + 20, 8, 128), 5.0, dtype=torch.float16, device="cuda")
+    kv = torch.ones(n, 2, 128, dtype=torch.float16, device="cuda")
+    outs = [torch.full((n + 20, 2, 128), 5.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    cache = engine.Kv4Cache(prob, pool=w["kv4_pool"])
+    for off in ([0, 30, 10, 35, 40], [-5, 10, 20, 90, 40], [40, 30, 20, 10, 0],
+                [0, 2 ** 31 - 1, -2 ** 31, 7, 40]):
+        say(f"[offsets] {off}")
+        to = torch.tensor(off, dtype=torch.int32, device="cuda")
+        _context.pkv_prompt_kv4(prob, None, to, n, w["seq_lens"], 1, w["q"], w["kv4_pool"],
+                                w["block_table"], None, out[10:10 + n])
+        _context.pkv_kv4_load(prob, to, n, w["seq_lens"], w["block_table"], w["kv4_pool"],
+                              outs[0][10:10 + n], outs[1][10:10 + n])
+        cache.store(kv, kv, w["block_table"], w["seq_lens"], to)
+        torch.cuda.synchronize()
+        for t in (out, *outs):
+            assert (t[:10] == 5).all() and (t[10 + n:] == 5).all()
