@@ -23,7 +23,9 @@
  * outside [0, num_pool_pages) holds no tokens (they are not stored, not seen,
  * and not read back); offsets outside [0, num_tokens] are clamped to it.  A
  * query that sees nothing gets out = 0, lse = -inf.  Tokens that no query of
- * a row sees may hold anything, NaN and infinities included.
+ * a row sees may hold anything, NaN and infinities included; a NaN or an
+ * infinity in a token that one query of a row sees may also reach other queries
+ * of that row (never other rows).
  *
  * 4-bit cache (kv4).  K and V share one pool, bytes
  *     kv4_pool [num_pool_pages][Hkv][17 d],
@@ -96,19 +98,20 @@ pkv_status pkv_kv4_load(const pkv_problem* prob, const int32_t* tok_offsets, int
  * read.  Each row's list of visible pages is cut into up to max_splits equal
  * ranges, max(1, ceil(T_max / max_splits)) pages each with T_max the longest
  * row's list.
- *   workspace: pkv_attend_workspace_bytes(prob, max_splits) bytes of device
- *     memory, 16-byte aligned, all zero before the first call that uses it
- *     and left reusable by every call.  Calls that overlap on one workspace
- *     race, two replays of captured graphs included; results do not depend
- *     on what an earlier call left there.
+ *   workspace: at least pkv_attend_workspace_bytes(prob, max_splits) bytes of
+ *     device memory, 16-byte aligned, the first 256 KiB (one counter for each of
+ *     65536 pairs of row and KV head) zero before the first call that uses it;
+ *     every call leaves them zero.  Calls of any problems, prompts included, may use
+ *     one workspace in turn; calls that overlap on it race, two replays of
+ *     captured graphs included.
  *   out [B][Hq][d], lse [B][Hq] (may be NULL) as in pkv.h; softmax statistics
  *     and sums are held in fp32.
  * pkv_problem.kernel is ignored.  Every G <= 16 is covered at both head sizes.
  * Errors: PKV_EINVAL (null pointer, a window or sinks < 0, max_splits outside
  * [1, 65535]), PKV_ESHAPE (problem, a misaligned pointer), PKV_EDTYPE,
  * PKV_ENOSPC (workspace too small), PKV_ERANGE (B or Hq above 65535, more than
- * 2^24 - 1 tasks B * Hkv * max_splits, or B * Hq above that), PKV_EHIP.
- * pkv_attend_workspace_bytes gives 0 where the call would be refused.
+ * 2^24 - 1 tasks B * Hkv * max_splits, or more than 65536 pairs B * Hkv in more
+ * than one split), PKV_EHIP.  pkv_attend_workspace_bytes gives 0 where the call would be refused.
  */
 size_t pkv_attend_workspace_bytes(const pkv_problem* prob, int32_t max_splits);
 pkv_status pkv_attend_window(const pkv_problem* prob, const pkv_view* view,
@@ -145,8 +148,8 @@ int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* view, int32_t
  *     where the call would be refused), on the terms of pkv_attend_window's;
  *     one_per_row says that the call passes no tok_offsets.
  * Errors: PKV_EINVAL, PKV_ESHAPE, PKV_EDTYPE, PKV_ENOSPC as above, PKV_ERANGE
- * (more than 2^24 - 1 workgroups: (num_tokens * G / 128 + B) * Hkv *
- * max_splits), PKV_EHIP.
+ * (more than 2^24 - 1 workgroups (num_tokens * G / 128 + B) * Hkv * max_splits, or
+ * more than 65536 tiles of KV heads in splits), PKV_EHIP.
  */
 size_t pkv_prompt_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
                                   int32_t one_per_row, int32_t max_splits);

@@ -48,8 +48,12 @@ int64_t attend_slots(const pkv_problem* p, int32_t splits) {
   return int64_t(p->batch) * p->num_kv_heads * splits;
 }
 
-// Workspace: arrivals, then (m, l) of every slot, then o, each part 256-byte
-// aligned.
+// Workspace of both attention calls: the arrival counters, at one place for every
+// problem, so that calls of any sizes find them as zero as the last one left
+// them; then the states (decode: (m, l) of every slot, then o).
+constexpr int64_t kCounters = 65536;
+constexpr size_t kCounterBytes = kCounters * sizeof(int32_t);
+
 struct Workspace {
   size_t ml, o, bytes;
 };
@@ -59,7 +63,7 @@ Workspace workspace_of(const pkv_problem* p, int32_t splits) {
   const size_t slots = static_cast<size_t>(attend_slots(p, splits));
   const size_t g = static_cast<size_t>(p->num_q_heads / p->num_kv_heads);
   Workspace w;
-  w.ml = up(size_t(p->batch) * p->num_kv_heads * sizeof(int32_t));
+  w.ml = kCounterBytes;
   w.o = w.ml + up(slots * g * 2 * sizeof(float));
   w.bytes = w.o + slots * g * p->head_dim * sizeof(float);
   return w;
@@ -74,11 +78,10 @@ pkv_status check_run(const pkv_problem* prob, const int32_t* tok_offsets, int32_
   return PKV_OK;
 }
 
-// Rows are the third grid dimension of the attention launch, query heads the
-// first and rows the second of the join.
+// Rows are the third grid dimension of the launch; pairs in splits take a counter.
 pkv_status check_attend_size(const pkv_problem* p, int32_t splits) {
   if (p->batch > 65535 || p->num_q_heads > 65535 || attend_slots(p, splits) > kMaxGridGroups ||
-      int64_t(p->batch) * p->num_q_heads > kMaxGridGroups)
+      (splits > 1 && int64_t(p->batch) * p->num_kv_heads > kCounters))
     return PKV_ERANGE;
   return PKV_OK;
 }
@@ -126,17 +129,15 @@ pkv_status attend(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   return launch_attend(*prob, kv4, a, stream);
 }
 
-// Workspace of a split prompt: arrivals, then the states.
-struct PromptWorkspace {
-  size_t state, bytes;
-};
+// Launch size of a prompt, and its counters where it is split.
+bool prompt_fits(const pkv_problem* p, int64_t tiles, int32_t splits) {
+  const int64_t pairs = tiles * p->num_kv_heads;
+  return pairs * splits <= kMaxGridGroups && (splits == 1 || pairs <= kCounters);
+}
 
-PromptWorkspace prompt_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits) {
-  const size_t pairs = static_cast<size_t>(tiles) * p->num_kv_heads;
-  PromptWorkspace w;
-  w.state = (pairs * sizeof(int32_t) + 255) & ~size_t(255);
-  w.bytes = w.state + pairs * splits * prompt_state_floats(p->head_dim) * sizeof(float);
-  return w;
+size_t prompt_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits) {
+  return kCounterBytes + static_cast<size_t>(tiles) * p->num_kv_heads * splits *
+                             prompt_state_floats(p->head_dim) * sizeof(float);
 }
 
 pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* tok_offsets,
@@ -152,7 +153,8 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   if (num_tokens == 0) return PKV_OK;
   if (!q || !k_pool || (!kv4 && !v_pool) || !out || (max_splits > 1 && !workspace))
     return PKV_EINVAL;
-  if (!aligned(workspace, 16) || !aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 16))
     return PKV_ESHAPE;
   PromptArgs a{};
   a.q = q;
@@ -175,12 +177,11 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   set_scale(prob, &a);
   a.splits = max_splits;
   const int64_t tiles = prompt_tiles(a);
-  if (tiles * a.num_kv_heads * max_splits > kMaxGridGroups) return PKV_ERANGE;
+  if (!prompt_fits(prob, tiles, max_splits)) return PKV_ERANGE;
   if (max_splits > 1) {
-    const PromptWorkspace w = prompt_workspace_of(prob, tiles, max_splits);
-    if (workspace_bytes < w.bytes) return PKV_ENOSPC;
+    if (workspace_bytes < prompt_workspace_of(prob, tiles, max_splits)) return PKV_ENOSPC;
     a.arrivals = static_cast<int32_t*>(workspace);
-    a.state = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.state);
+    a.state = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
   }
   return launch_prompt(*prob, kv4, a, stream);
 }
@@ -346,10 +347,10 @@ int64_t tiles_of(const pkv_problem* p, int32_t num_tokens, int32_t one_per_row) 
 extern "C" size_t pkv_prompt_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
                                              int32_t one_per_row, int32_t max_splits) {
   const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
-  if (tiles < 0 || max_splits < 1 || max_splits > 65535 ||
-      tiles * prob->num_kv_heads * max_splits > kMaxGridGroups || max_splits == 1)
+  if (tiles < 0 || max_splits < 2 || max_splits > 65535 ||
+      !prompt_fits(prob, tiles, max_splits))
     return 0;
-  return prompt_workspace_of(prob, tiles, max_splits).bytes;
+  return prompt_workspace_of(prob, tiles, max_splits);
 }
 
 extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* view,

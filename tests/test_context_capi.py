@@ -192,3 +192,18 @@ def test_token_strides_are_checked_by_the_binding():
         _context.token_stride(x.transpose(1, 2)[:, 0])
     with pytest.raises(ValueError):
         _context.token_stride(x[..., ::2][:, 0])
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_counters_of_split_calls(kv4):
+    """Pairs of row (or tile) and KV head in splits: one counter each, 65536 of
+    them, at one place for every problem; one split takes none."""
+    many = _prob(batch=9000, num_q_heads=8, num_kv_heads=8)
+    assert _attend(kv4, prob=many, ws_bytes=1 << 60) == PKV_ERANGE
+    assert _context.pkv_attend_workspace_bytes(many, 4) == 0
+    assert _context.pkv_attend_workspace_bytes(many, 1) > 0
+    assert _prompt(kv4, splits=2, n=1 << 20, ws=P, ws_bytes=1 << 60,
+                   prob=_prob(num_q_heads=8, num_kv_heads=8)) == PKV_ERANGE  # 65552 pairs
+    assert _context.pkv_attend_workspace_bytes(_prob(), 4) >= (256 << 10) + 16 * 4 * 130 * 4
+    assert (_context.pkv_prompt_workspace_bytes(_prob(), 10, False, 3)
+            >= (256 << 10) + 2 * 2 * 3 * 128 * 130 * 4)

@@ -663,3 +663,33 @@ def test_unordered_offsets_stay_in_bounds():
         torch.cuda.synchronize()
         for t in (out, *outs):
             assert (t[:10] == 5).all() and (t[10 + n:] == 5).all()
+
+
+def test_one_workspace_for_problems_of_all_sizes():
+    """Calls of different batches, splits and kinds use one workspace in turn,
+    each finding its counters at zero."""
+    shapes = [dict(lens=[900, 33], splits=40, hkv=2), dict(lens=[100] * 60, splits=3, hkv=8),
+              dict(lens=[700], splits=100, hkv=1), dict(lens=[90, 300], new=[90, 40], splits=4, hkv=3)]
+    steps = []
+    for i, s in enumerate(shapes):
+        b = Batch(i, s["lens"], s.get("new"), hkv=s["hkv"], group=2, d=64)
+        step = (engine.PromptStep(b.problem(), int(b.new.sum()), 0, 0, s["splits"])
+                if "new" in s else _step(b, s["splits"]))
+        steps.append((b, step, b.device(), "new" in s))
+    shared = torch.zeros(max(s.workspace.numel() for _, s, _, _ in steps), dtype=torch.uint8,
+                         device="cuda")
+    for _ in range(2):
+        for b, step, w, many in steps + steps[::-1]:
+            say(f"[shared workspace] B={len(b.lens)} Hkv={b.hkv} splits={step.splits}")
+            head = (b.problem(), step.view)
+            if many:
+                _context.pkv_prompt_window(*head, w["tok_offsets"], step.num_tokens, w["seq_lens"],
+                                           step.splits, w["q"], w["k_pool"], w["v_pool"],
+                                           w["block_table"], shared, step.out, step.lse)
+            else:
+                _context.pkv_attend_window(*head, w["seq_lens"], step.splits, w["q"], w["k_pool"],
+                                           w["v_pool"], w["block_table"], shared, step.out,
+                                           step.lse)
+            torch.cuda.synchronize()
+            check(step.out, step.lse, b.reference(), "f16", 64, b.vmax, many, "shared workspace")
+            assert not shared[:256 << 10].any()
