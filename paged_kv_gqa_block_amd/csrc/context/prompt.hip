@@ -239,17 +239,15 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
     }
   };
   // Clear the V rows of this wave's page of step s that no query of the tile
-  // sees: they may hold anything, and 0 * NaN is not 0.  After the page has
-  // landed, before the others read it.
+  // sees, all of them where there is no page: they may hold anything, and 0 *
+  // NaN is not 0.  After the page has landed, before the others read it.
   auto clear_unseen = [&](int id, int s, Tile& vt) __attribute__((always_inline)) {
     const int b0 = base_of(s);
-    const bool all = id < 0 || (b0 + 15 <= p_last &&
-                                (p_first - b0 < window || b0 + 15 < a.sinks));
-    if (all) return;
+    if (id >= 0 && b0 + 15 <= p_last && (p_first - b0 < window || b0 + 15 < a.sinks)) return;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int t = b0 + KPL * i + lk;
-      if (t > p_last || (p_first - t >= window && t >= a.sinks))
+      if (id < 0 || t > p_last || (p_first - t >= window && t >= a.sinks))
         vt[16 * wave + KPL * i + lk][lc] = zero4();
     }
   };
