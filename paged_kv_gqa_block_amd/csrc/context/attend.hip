@@ -22,6 +22,16 @@
 //    fp32 and fit in f16.
 // Three waves of a SIMD (at most 168 registers): with the compiler's own two,
 // 96 rows x 8 heads x 8192 tokens in 4 bits took 190 us instead of 160.
+// Joining in the same launch: one row of 32768 tokens in 4 bits, 8 KV heads,
+// took 18.1 us with a second launch and 17.0 us so, and the host one call less
+// (16 -> 9 us).
+//
+// Measured (G = 8, d = 128, 64 rows, 8 KV heads, bf16): 4 bits, 1.1 million
+// tokens (1.21 GB): 234 us, 5.2 TB/s; the same pages read and not used take
+// 187 us (6.5 TB/s), the rest is conversion and matrix work that three waves do
+// not hide.  16 bits, window 1000 and 5 sinks (260 MB): 44 us, 5.9 TB/s; window
+// 4096 over eight rows (134 MB): 27 us, 5.0 TB/s.  Small calls: 7 us, a chain of
+// dependent loads (length, page number, page, state, counter).
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
@@ -131,7 +141,8 @@ __device__ __forceinline__ f32x4 pv(const uint32_t (&p)[4], const uint32_t (&v)[
 }
 
 template <int D, bool BF16, bool KV4, int GP, int NW, int PF>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3,8))) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3, 8)))
+void attend_kernel(AttendArgs a) {
   constexpr int UP = KV4 ? 2 : 1;  // pages per unit
   constexpr int VEC = D / 16;      // channels per lane
   constexpr int NT = D / 32;       // score products per page

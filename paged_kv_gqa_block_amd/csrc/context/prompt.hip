@@ -26,6 +26,16 @@
 // relative 2^-8 (bf16) or 2^-11 (f16) at most each, of the size of the output's
 // own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
 // last rounding.
+//
+// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 397-415 us
+// for 413 GFLOP, 1.0 PFLOP/s, 0.84 of what a square product of 8192 reaches on
+// the same card.  Matrix work fills half of a SIMD's cycles and vector work
+// (exponentials, maxima, rounding) 45 %, and the two hardly overlap.  Direct
+// loads and two scores in flight brought it from 502 us; deeper rings of buffers,
+// pages touched ahead in L2 (430 us), wave priorities and tiles of 64 rows
+// brought nothing.  Eight chunks of 9-54 tokens behind a window of 4096, 64
+// heads over 8: 75 us; 20 tiles of 65 steps a KV head do not fill the card
+// evenly, and each further split writes and reads 65 KiB of state a tile.
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
