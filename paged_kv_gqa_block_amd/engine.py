@@ -187,6 +187,7 @@ class _ContextCalls:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.dtype = torch.bfloat16 if prob.dtype == _lib.PKV_BF16 else torch.float16
         self.kv4_page_bytes = _context.pkv_kv4_page_bytes(prob.head_dim)
 
@@ -202,7 +203,7 @@ class _ContextCalls:
     def _stream(self, stream) -> int:
         if stream is not None:
             return stream if isinstance(stream, int) else stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
         """The address of `t`, after its checks."""
@@ -248,7 +249,7 @@ class _ContextCalls:
         """Call an entry point (every argument a number or a reference) with
         the buffers' device current."""
         call = getattr(_lib.LIB, fn)
-        if torch.cuda.current_device() == self.device.index:
+        if torch._C._cuda_getDevice() == self._index:
             status = call(self._prob_ref, *args)
         else:
             with torch.cuda.device(self.device):
