@@ -170,6 +170,7 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   a.num_q_heads = prob->num_q_heads;
   a.num_kv_heads = prob->num_kv_heads;
   a.group = prob->num_q_heads / prob->num_kv_heads;
+  a.group_inv = static_cast<uint32_t>(ceil_div(4096, a.group));
   a.max_pages = prob->max_pages_per_row;
   a.num_pool_pages = prob->num_pool_pages;
   a.window = clean_window(prob, view);

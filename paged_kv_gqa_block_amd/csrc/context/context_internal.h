@@ -80,6 +80,7 @@ struct PromptArgs {
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t group;
+  uint32_t group_inv;   // ceil(4096 / group)
   int32_t max_pages;
   int32_t num_pool_pages;
   int32_t splits;

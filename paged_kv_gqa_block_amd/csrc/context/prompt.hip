@@ -46,7 +46,6 @@ namespace pkv {
 namespace {
 
 constexpr int kKeys = 64;             // keys per step: four pages, one per wave
-constexpr int kNoPage = 0x7ffffff0;   // token base of an absent page: behind every query
 
 // Physical 16-byte chunk of chunk ch of key t.  K is read 32 keys at a time at
 // one chunk, V four keys at a time over 64 bytes: in both, lanes that are
@@ -112,13 +111,19 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const int r0 = k_tile * kTileRows;
   const int rows = static_cast<int>(min(rows64 - r0, int64_t(kTileRows)));  // of this tile
   const int shift = run.len - run.count;  // position of the run's first token
-  const int p_first = max(shift + r0 / G, 0);  // negative positions see nothing
-  const int p_last = shift + (r0 + rows - 1) / G;
+  // Token of the tile's row r, 0 <= r < 128, in the run: x / G = x ceil(4096 / G) /
+  // 4096 for x < 144 and G <= 16, as the product is off by less than 4096 / G.
+  const int j0 = r0 / G, head0 = r0 - j0 * G;
+  auto token_of = [&](int r) {
+    return j0 + static_cast<int>(static_cast<uint32_t>(head0 + r) * a.group_inv >> 12);
+  };
+  const int p_first = max(shift + j0, 0);  // negative positions see nothing
+  const int p_last = shift + token_of(rows - 1);
 
   // This lane's query.
   const int wr = 32 * wave;  // the wave's first row in the tile
   const int my = wr + n;
-  const int j = (r0 + min(my, rows - 1)) / G;
+  const int j = token_of(min(my, rows - 1));
   const int head = (r0 + min(my, rows - 1)) - j * G;
   const int p = max(shift + j, -1);
   const int64_t qh = (int64_t(run.first) + j) * a.num_q_heads + g * G + head;
@@ -140,21 +145,11 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   if (s_begin >= s_end) return;
   const int32_t* bt = a.block_table + int64_t(run.row) * a.max_pages;
 
-  // B operand of the scores: channels 16 t + 8 h .. of this lane's query.
-  uint4 qf[NQ];
-  {
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qh * D + 8 * h;
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      qf[t] = mine ? load16(qp + 16 * t) : zero4();
-      qf[t].x ^= a.q_flip, qf[t].y ^= a.q_flip, qf[t].z ^= a.q_flip, qf[t].w ^= a.q_flip;
-    }
-  }
   // Steps whose every key is seen by every query of the wave (absent pages
   // aside): those behind the start of the last query's window and before the
   // first query's position, or those before the end of the sinks.
-  const int pw_first = max(shift + (r0 + min(wr, rows - 1)) / G, -1);
-  const int pw_last = max(shift + (r0 + min(wr + 31, rows - 1)) / G, -1);
+  const int pw_first = max(shift + token_of(min(wr, rows - 1)), -1);
+  const int pw_last = max(shift + token_of(min(wr + 31, rows - 1)), -1);
   int full_lo = 0;
   if (a.window > 0) {
     const int w0 = max(pw_last - a.window + 1, 0);           // first token all of them see
@@ -170,6 +165,15 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
     const int id = v < sp.count ? bt[v < sp.ahead ? v : v + sp.skip] : -1;
     return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pool_pages) ? id : -1;
   };
+  int ids0 = s_begin, ids = load_ids(s_begin), ids_next = load_ids(s_begin + 16);
+  // B operand of the scores: channels 16 t + 8 h .. of this lane's query (lanes
+  // behind the tile's rows repeat its last one).
+  uint4 qf[NQ];
+  {
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qh * D + 8 * h;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) qf[t] = load16(qp + 16 * t);
+  }
   auto base_of = [&](int s) {
     const int v = 4 * s + wave;
     return 16 * (v < sp.ahead ? v : v + sp.skip);
@@ -290,20 +294,25 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
         s[sub] = mfma32<BF16>(kt[key][k_chunk<D>(key, 2 * t + h)], qf[t], s[sub]);
       }
   };
-  // `bad`: this step has absent pages (a bit each).
+  // `bad`: this step has absent pages (a bit each).  The tokens of a page that
+  // this lane's query sees, a bit each: below p + 1 and not below the window's
+  // start, or below the sinks' end.
   auto mask = [&](int st, uint32_t bad, f32x16 (&s)[2]) {
+    const int lo = max(p + 1 - window, 0), sink = min(a.sinks, p + 1);
+    auto below = [](int n) { return (1u << min(max(n, 0), 16)) - 1u; };
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
+    for (int x = 0; x < 4; ++x) {
+      const int v = 4 * st + x;
+      const int b0 = 16 * (v < sp.ahead ? v : v + sp.skip);
+      uint32_t seen = (below(p + 1 - b0) & ~below(lo - b0)) | below(sink - b0);
+      seen = ((bad >> x) & 1) ? 0u : seen >> (4 * h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int x = 2 * sub + (i >> 3), v = 4 * st + x;
-        const int b0 = ((bad >> x) & 1) ? kNoPage : 16 * (v < sp.ahead ? v : v + sp.skip);
-        const int t = b0 + 8 * ((i >> 2) & 1) + 4 * h + (i & 3);
-        // t > p wraps to a large unsigned number
-        const bool ok = (static_cast<uint32_t>(p - t) < static_cast<uint32_t>(window)) |
-                        (t < min(a.sinks, p + 1));
-        if (!ok) s[sub][i] = kNegInf;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t keep = __builtin_amdgcn_sbfe(seen, 8 * (i >> 2) + (i & 3), 1);
+        const uint32_t e = __float_as_uint(s[x >> 1][8 * (x & 1) + i]);
+        s[x >> 1][8 * (x & 1) + i] = __uint_as_float((e & keep) | (0xff800000u & ~keep));
       }
+    }
   };
   const int kq = (lane & 15) >> 2, cq = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   auto softmax_pv = [&](const Tile& vt, const f32x16 (&s)[2]) __attribute__((always_inline)) {
@@ -356,7 +365,6 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
 
   // ---- the walk -----------------------------------------------------------------------
   // During step s, K of step s + 2 and V of step s + 1 are under way.
-  int ids0 = s_begin, ids = load_ids(s_begin), ids_next = load_ids(s_begin + 16);
   uint64_t no_page = __builtin_amdgcn_ballot_w64(ids < 0);
   // This wave's page of a step, and the step's absent pages (a bit each).
   struct StepPages {
@@ -384,6 +392,9 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   issue_k(pg1.id, s_begin + 1, kt1);
   put_k(kt1);
   put_v(vt0);
+#pragma unroll
+  for (int t = 0; t < NQ; ++t)
+    qf[t].x ^= a.q_flip, qf[t].y ^= a.q_flip, qf[t].z ^= a.q_flip, qf[t].w ^= a.q_flip;
   landed();
   clear_unseen(pg0.id, s_begin, vt0);
   __syncthreads();
