@@ -363,8 +363,13 @@ extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* vi
   if (tiles < 0 || check_view(view) != PKV_OK || num_cus < 1 || num_cus > 1024) return 0;
   if (tiles == 0) return 1;
   // Two workgroups a compute unit, as long as a split keeps eight steps of four
-  // pages.
-  const int64_t fill = 2 * int64_t(num_cus) / (tiles * prob->num_kv_heads);
+  // pages.  Tiles: half of a row's last one on the average; the launch counts the
+  // real ones and cuts into fewer ranges where there are more.
+  const int64_t rows = int64_t(num_tokens) * (prob->num_q_heads / prob->num_kv_heads);
+  const int64_t likely = one_per_row ? tiles
+                                     : std::max(ceil_div(rows, kTileRows),
+                                                rows / kTileRows + prob->batch / 2);
+  const int64_t fill = 2 * int64_t(num_cus) / (likely * prob->num_kv_heads);
   const int64_t keys = std::min<int64_t>(most_pages(prob, view) + ceil_div(num_tokens, 16),
                                          prob->max_pages_per_row);
   return static_cast<int32_t>(std::max<int64_t>(1, std::min(fill, keys / 32)));

@@ -77,7 +77,7 @@ __device__ __forceinline__ uint2 read_transposed(const void* p) {
 }
 
 template <int D, bool BF16, bool KV4>
-__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles) {
+__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles, int slots) {
   constexpr int NQ = D / 16;   // products over the channels
   constexpr int NC = D / 32;   // channel blocks of the output
   constexpr int CH = D / 8;    // 16-byte chunks of a key
@@ -93,21 +93,15 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const int n = lane & 31, h = lane >> 5;
   const int g = blockIdx.x % a.num_kv_heads;
   const int ts = blockIdx.x / a.num_kv_heads;
-  const int split = ts % a.splits;
-  // Late tiles of a causal row see the most keys: they start first.
-  const int item = tiles - 1 - ts / a.splits;
   const int G = a.group;
 
-  int k_tile = 0;
-  Run run;
-  if (a.tok_offsets) {
-    run = find_run(a, item, [&](int64_t off, int64_t r) { return tile_base(off, r, G); });
-    k_tile = item - static_cast<int>(tile_base(run.first, run.row, G));
-  } else {
-    run = single_run(a, item);
-  }
+  const TileRun found = find_tile(a, ts, tiles, slots);
+  const int k_tile = found.tile, splits = found.splits;
+  if (k_tile < 0) return;
+  const Run& run = found.run;
+  const int item = ts / splits, split = ts - item * splits;
   const int64_t rows64 = int64_t(run.count) * G;
-  if (k_tile < 0 || int64_t(k_tile) * kTileRows >= rows64) return;
+  if (int64_t(k_tile) * kTileRows >= rows64) return;
   const int r0 = k_tile * kTileRows;
   const int rows = static_cast<int>(min(rows64 - r0, int64_t(kTileRows)));  // of this tile
   const int shift = run.len - run.count;  // position of the run's first token
@@ -140,7 +134,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
   const int window = a.window > 0 ? a.window : 0x7fffffff;
   const SeenPages sp = seen_pages(p_first, p_last, a.window, a.sinks);
   const int all_steps = (sp.count + 3) >> 2;
-  const int per_split = (all_steps + a.splits - 1) / a.splits;
+  const int per_split = (all_steps + splits - 1) / splits;
   const int s_begin = split * per_split, s_end = min(s_begin + per_split, all_steps);
   if (s_begin >= s_end) return;
   const int32_t* bt = a.block_table + int64_t(run.row) * a.max_pages;
@@ -489,11 +483,14 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles)
 }
 
 template <int D, bool BF16>
-void launch_fmt(bool kv4, const PromptArgs& a, int tiles, uint32_t grid, hipStream_t s) {
+void launch_fmt(bool kv4, const PromptArgs& a, int tiles, int slots, uint32_t grid,
+                hipStream_t s) {
   if (kv4)
-    hipLaunchKernelGGL((prompt_kernel<D, BF16, true>), dim3(grid), dim3(256), 0, s, a, tiles);
+    hipLaunchKernelGGL((prompt_kernel<D, BF16, true>), dim3(grid), dim3(256), 0, s, a, tiles,
+                       slots);
   else
-    hipLaunchKernelGGL((prompt_kernel<D, BF16, false>), dim3(grid), dim3(256), 0, s, a, tiles);
+    hipLaunchKernelGGL((prompt_kernel<D, BF16, false>), dim3(grid), dim3(256), 0, s, a, tiles,
+                       slots);
 }
 
 }  // namespace
@@ -502,12 +499,21 @@ pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hi
   const int64_t tiles = prompt_tiles(a);
   const bool bf = p.dtype == PKV_BF16;
   const uint32_t n = static_cast<uint32_t>(tiles * a.num_kv_heads * a.splits);
+  // Workgroups a KV head that run at the same time: two a compute unit.
+  int slots = 0;
+  if (a.splits > 1) {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+      return PKV_EHIP;
+    slots = 2 * cus / a.num_kv_heads;
+  }
   if (p.head_dim == 128) {
-    if (bf) launch_fmt<128, true>(kv4, a, static_cast<int>(tiles), n, s);
-    else launch_fmt<128, false>(kv4, a, static_cast<int>(tiles), n, s);
+    if (bf) launch_fmt<128, true>(kv4, a, static_cast<int>(tiles), slots, n, s);
+    else launch_fmt<128, false>(kv4, a, static_cast<int>(tiles), slots, n, s);
   } else {
-    if (bf) launch_fmt<64, true>(kv4, a, static_cast<int>(tiles), n, s);
-    else launch_fmt<64, false>(kv4, a, static_cast<int>(tiles), n, s);
+    if (bf) launch_fmt<64, true>(kv4, a, static_cast<int>(tiles), slots, n, s);
+    else launch_fmt<64, false>(kv4, a, static_cast<int>(tiles), slots, n, s);
   }
   return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
 }

@@ -61,6 +61,88 @@ __device__ __forceinline__ Run single_run(const Args& a, int row) {
   return make_run(row, row, row + 1, a.seq_lens[row], a.max_pages);
 }
 
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int sh = 1; sh < 64; sh <<= 1) {
+    const int y = __builtin_amdgcn_ds_bpermute(((lane - sh) & 63) << 2, x);
+    x += lane >= sh ? y : 0;
+  }
+  return x;
+}
+
+// Query tiles of a prompt: row after row, the late tiles of a row first.
+// Counted from the offsets, not from the bound that sizes the grid: launched
+// workgroups without a tile then all lie behind the others, which come out even
+// on the compute units.
+struct TileRun {
+  Run run;
+  int tile;    // of the run; negative: none
+  int splits;  // ranges that every tile's keys are cut into
+};
+
+// The share of workgroup `ts` of one KV head.  With max_splits > 1 the tiles are
+// counted first, so that tiles times ranges fill `slots` workgroups a KV head
+// and no more.
+template <typename Args>
+__device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, int slots) {
+  const int lane = threadIdx.x & 63;
+  TileRun t;
+  t.tile = -1;
+  t.splits = a.splits;
+  if (!a.tok_offsets) {
+    if (a.splits > 1) t.splits = min(a.splits, max(slots / a.batch, 1));
+    const int row = ts / t.splits;
+    if (row < a.batch) {
+      t.run = single_run(a, row);
+      t.tile = 0;
+    }
+    return t;
+  }
+  int first, next, len, count;
+  auto load = [&](int r0) {  // 64 rows from r0 on; count: tiles up to and with a lane's row
+    const int r = r0 + lane;
+    first = a.tok_offsets[min(r, a.batch)];
+    next = a.tok_offsets[min(r + 1, a.batch)];
+    len = a.seq_lens[min(r, a.batch - 1)];
+    asm volatile("" : "+v"(first), "+v"(next), "+v"(len));  // one wait for the three
+    first = clamp_offset(first, a.num_tokens), next = clamp_offset(next, a.num_tokens);
+    const int64_t rows = int64_t(max(next - first, 0)) * a.group;
+    count = wave_scan(r < a.batch ? static_cast<int>((rows + kTileRows - 1) / kTileRows) : 0);
+  };
+  load(0);
+  if (a.splits > 1) {
+    int total = __builtin_amdgcn_readlane(count, 63);
+    if (a.batch > 64) {
+      for (int r0 = 64; r0 < a.batch; r0 += 64) {
+        load(r0);
+        total += __builtin_amdgcn_readlane(count, 63);
+      }
+      load(0);
+    }
+    t.splits = min(a.splits, max(slots / max(total, 1), 1));
+  }
+  const int item = ts / t.splits;
+  if (item >= tiles) return t;
+  for (int r0 = 0, before = 0;;) {
+    const int in_all = __builtin_amdgcn_readlane(count, 63);
+    if (item < before + in_all) {
+      const uint64_t past = __builtin_amdgcn_ballot_w64(before + count > item);
+      const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+      t.run = make_run(r0 + at, __builtin_amdgcn_readlane(first, at),
+                       __builtin_amdgcn_readlane(next, at), __builtin_amdgcn_readlane(len, at),
+                       a.max_pages);
+      t.tile = before + __builtin_amdgcn_readlane(count, at) - 1 - item;
+      return t;
+    }
+    before += in_all;
+    r0 += 64;
+    if (r0 >= a.batch) return t;
+    load(r0);
+  }
+}
+
 // A page's share of a run: tokens [begin, end) of block-table entry `entry`
 // (begin >= end: none), as positions.
 struct Segment {
