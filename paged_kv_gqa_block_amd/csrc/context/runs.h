@@ -36,10 +36,8 @@ __device__ __forceinline__ Run find_run(const Args& a, int64_t item, Base base) 
   int below = 0, off = 0, len = 0, r0 = 0;
   for (;; r0 += 64) {
     const int r = r0 + lane;
-    off = a.tok_offsets[min(r, a.batch)];
-    len = a.seq_lens[min(r, a.batch - 1)];
-    asm volatile("" : "+v"(off), "+v"(len));  // one wait for both loads
-    off = r <= a.batch ? clamp_offset(off, a.num_tokens) : a.num_tokens;
+    off = r <= a.batch ? clamp_offset(a.tok_offsets[r], a.num_tokens) : a.num_tokens;
+    len = r < a.batch ? a.seq_lens[r] : 0;
     const bool in = r < a.batch && base(off, r) <= item;
     const int k = __popcll(__builtin_amdgcn_ballot_w64(in));
     below += k;
