@@ -693,3 +693,59 @@ def test_one_workspace_for_problems_of_all_sizes():
             torch.cuda.synchronize()
             check(step.out, step.lse, b.reference(), "f16", 64, b.vmax, many, "shared workspace")
             assert not shared[:256 << 10].any()
+
+
+@pytest.mark.parametrize("rows", [64, 65, 130, 300])
+def test_prompt_splits_of_many_rows(rows):
+    """The launch counts the tiles of any number of rows before it chooses the
+    ranges; rows without new tokens between them."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, 400, rows)
+    new = np.minimum(lens, rng.integers(0, 40, rows) * (rng.random(rows) < 0.6))
+    say(f"[splits of many rows] {rows}")
+    b = Batch(rows, lens, new, hkv=1, group=8, d=64, dtype="bf16", window=300, sinks=3)
+    w = b.device()
+    step = engine.PromptStep(b.problem(), int(new.sum()), 300, 3, splits=6)
+    out, lse = step.run(w)
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "bf16", 64, b.vmax, True, f"{rows} rows")
+
+
+def test_prompt_split_replays_follow_the_offsets():
+    """A captured prompt whose rows change: other tile counts, so other ranges,
+    on one workspace; one token a row without offsets too."""
+    b = Batch(31, [2000, 1500, 900, 60], [60, 1, 33, 60], hkv=1, group=4, d=128)
+    w = b.device()
+    n = int(b.new.sum())
+    step = engine.PromptStep(b.problem(), n, 0, 0, splits=64)
+    step.run(w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run(w)
+    for new in ([60, 1, 33, 60], [0, 0, 154, 0], [100, 54, 0, 0], [1, 1, 1, 1], [0, 0, 0, 60]):
+        say(f"[replay] new tokens {new}")
+        off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        w["tok_offsets"].copy_(torch.from_numpy(off))
+        step.out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = step.out.clone(), step.lse.clone()
+        one = engine.PromptStep(b.problem(), n, 0, 0, splits=1)
+        one.out.fill_(7)
+        one.run(w)
+        torch.cuda.synchronize()
+        m = int(off[-1])
+        assert (got[0][m:] == 7).all()
+        # The same sums in another order: both within a rounding of P and of the output.
+        err = (got[0][:m].double() - one.out[:m].double()).abs().max().item() if m else 0
+        assert err <= 4 * 2.0 ** -11 * b.vmax, err
+        assert not step.workspace[:256 << 10].any()
+    with pytest.raises(ValueError):
+        step.run(dict(w, tok_offsets=None))
+    alone = engine.PromptStep(b.problem(), 4, 0, 0, splits=64)
+    ones = Batch(31, [2000, 1500, 900, 60], [1, 1, 1, 1], hkv=1, group=4, d=128)
+    x = ones.device()
+    out, lse = alone.run(dict(x, tok_offsets=None))
+    torch.cuda.synchronize()
+    check(out, lse, ones.reference(), "f16", 128, ones.vmax, True, "one token a row")
