@@ -218,10 +218,17 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
         load_lds16(r, &vt[16 * wave + KPL * i][0], v_off, i * 1024);
     }
   };
+  // A lane number whose uses are computed where they stand: the LDS offsets of a
+  // conversion, kept over the loop instead, spilled (one prompt of 8192: 506 us).
+  auto lane_now = [&] {
+    int x = lane;
+    asm volatile("" : "+v"(x));
+    return x;
+  };
   // 4-bit: to LDS, converted.
   auto put_k = [&](Tile& kt) __attribute__((always_inline)) {
     if constexpr (KV4) {
-      const int kg = lane >> 4, t = 16 * wave + (lane & 15);
+      const int ln = lane_now(), kg = ln >> 4, t = 16 * wave + (ln & 15);
 #pragma unroll
       for (int b = 0; b < D / 32; ++b)
         kt[t][k_chunk<D>(t, 4 * b + kg)] =
@@ -230,10 +237,10 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   };
   auto put_v = [&](Tile& vt) __attribute__((always_inline)) {
     if constexpr (KV4) {
-      const int c = lane & 15;
+      const int ln = lane_now(), c = ln & 15;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 16 * wave + 4 * (lane >> 4) + i;
+        const int t = 16 * wave + 4 * (ln >> 4) + i;
         const float sc = kv4_scale((v4.vs >> (8 * i)) & 0xff);
         if constexpr (D == 128) {
           vt[t][v_chunk<D>(t, c)] = kv4_eight<BF16>(v4.v[i], sc);
@@ -252,11 +259,12 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   auto clear_unseen = [&](int id, int s, Tile& vt) __attribute__((always_inline)) {
     const int b0 = base_of(s);
     if (id >= 0 && b0 + 15 <= p_last && (p_first - b0 < window || b0 + 15 < a.sinks)) return;
+    const int ln = lane_now();
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int t = b0 + KPL * i + lk;
+      const int r = KPL * i + ln / CH, t = b0 + r;
       if (id < 0 || t > p_last || (p_first - t >= window && t >= a.sinks))
-        vt[16 * wave + KPL * i + lk][lc] = zero4();
+        vt[16 * wave + r][ln % CH] = zero4();
     }
   };
 
@@ -400,9 +408,15 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   auto step = [&](int s, Tile& k_cur, Tile& k_next, Tile& v_cur, Tile& v_next, f32x16 (&sc)[2],
                   f32x16 (&sn)[2]) __attribute__((always_inline)) {
     const StepPages pg2 = pages_of(s + 2);
-    issue_k(pg2.id, s + 2, k_cur);
-    issue_v(pg1.id, s + 1, v_next);
+    if constexpr (!KV4) {
+      issue_k(pg2.id, s + 2, k_cur);
+      issue_v(pg1.id, s + 1, v_next);
+    }
     scores(k_next, sn);
+    if constexpr (KV4) {  // to registers: later, so that fewer are taken meanwhile
+      issue_k(pg2.id, s + 2, k_cur);
+      issue_v(pg1.id, s + 1, v_next);
+    }
     const bool full = (s >= full_lo && s < full_hi) || s < sink_hi;
     if (!full || pg0.bad) mask(s, pg0.bad, sc);
     softmax_pv(v_cur, sc);
