@@ -141,8 +141,9 @@ int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* view, int32_t
  * P enters the second product rounded to the problem's type; statistics and
  * sums are held in fp32.
  *   max_splits: a tile of 128 query rows (tokens times heads of a group) cuts
- *     its keys into up to this many ranges, for few queries over long contexts;
- *     1 needs no workspace.  pkv_prompt_splits gives a cap that fills num_cus
+ *     its keys into up to this many ranges, for few queries over long contexts,
+ *     and no more than fill the current device with the tiles there are; 1 needs
+ *     no workspace.  pkv_prompt_splits gives a cap that fills num_cus
  *     compute units (0 on an invalid argument).
  *   workspace: pkv_prompt_workspace_bytes device bytes (0 for one split and
  *     where the call would be refused), on the terms of pkv_attend_window's;

@@ -367,8 +367,8 @@ extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* vi
   // real ones and cuts into fewer ranges where there are more.
   const int64_t rows = int64_t(num_tokens) * (prob->num_q_heads / prob->num_kv_heads);
   const int64_t likely = one_per_row ? tiles
-                                     : std::max(ceil_div(rows, kTileRows),
-                                                rows / kTileRows + prob->batch / 2);
+                                     : std::max<int64_t>({1, ceil_div(rows, kTileRows),
+                                                          rows / kTileRows + prob->batch / 2});
   const int64_t fill = 2 * int64_t(num_cus) / (likely * prob->num_kv_heads);
   const int64_t keys = std::min<int64_t>(most_pages(prob, view) + ceil_div(num_tokens, 16),
                                          prob->max_pages_per_row);

@@ -207,3 +207,22 @@ def test_counters_of_split_calls(kv4):
     assert _context.pkv_attend_workspace_bytes(_prob(), 4) >= (256 << 10) + 16 * 4 * 130 * 4
     assert (_context.pkv_prompt_workspace_bytes(_prob(), 10, False, 3)
             >= (256 << 10) + 2 * 2 * 3 * 128 * 130 * 4)
+
+
+def test_split_caps_over_the_whole_range():
+    """No sizes, zero tokens and one row among them, end in anything but a cap
+    that the call accepts."""
+    for b in (1, 2, 3, 65, 65535):
+        for hq, hkv in ((1, 1), (16, 1), (8, 8), (64, 8), (4096, 4096)):
+            for pages in (1, 7, 41, 2048, (2 ** 31 - 1) // 16):
+                p = _prob(batch=b, num_q_heads=hq, num_kv_heads=hkv, max_pages_per_row=pages)
+                for view in (None, _context.make_view(1, 0), _context.make_view(2 ** 31 - 1, 5)):
+                    for cus in (1, 256, 1024):
+                        s = _context.pkv_attend_splits(p, view, cus)
+                        assert 1 <= s <= 1024
+                        assert s == 1 or b * hkv <= 65536
+                        for n in (0, 1, 2, 127, 129, 5000):
+                            s = _context.pkv_prompt_splits(p, view, n, False, cus)
+                            assert 1 <= s <= 2048
+                            assert s == 1 or _context.pkv_prompt_workspace_bytes(p, n, False, s)
+                        assert _context.pkv_prompt_splits(p, view, b, True, cus) >= 1
