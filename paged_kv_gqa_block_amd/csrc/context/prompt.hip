@@ -27,14 +27,14 @@
 // own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
 // last rounding.
 //
-// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 396-400 us
-// for 413 GFLOP, 1.04 PFLOP/s, 0.86 of what a square product of 8192 reaches on
+// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 396-412 us
+// for 413 GFLOP, 1.04 PFLOP/s, 0.83-0.86 of what a square product of 8192 reaches on
 // the same card (over 4 bits: 385 us).  Matrix work fills half of a SIMD's cycles
 // and vector work (exponentials, maxima, rounding) 45 %, and the two hardly
 // overlap.  Direct loads and two scores in flight brought it from 502 us; deeper
 // rings of buffers, pages touched ahead in L2 (430 us), wave priorities and tiles
 // of 64 rows brought nothing.  Eight chunks of 9-54 tokens behind a window of
-// 4096, 64 heads over 8: 61-65 us, of which 46 at the same rate, 8 until the first
+// 4096, 64 heads over 8: 61-66 us, of which 46 at the same rate, 8 until the first
 // pages are there (dependent loads) and 8 for the last join (65 KiB of state a
 // tile and range).  Eight prompts of 183-1659 tokens, d = 64, window 500: 20 us.
 #include "context_internal.h"

@@ -240,9 +240,12 @@ class _ContextCalls:
 
     def _new_tokens(self, name: str, t: torch.Tensor, n: int) -> tuple:
         """Address and token stride of new keys or values."""
-        if t.shape != (n, *self._shapes["token"]) or t.dtype != self.dtype or \
-                t.device != self.device:
+        heads, d = self._shapes["token"]
+        if t.shape != (n, heads, d) or t.dtype != self.dtype or t.device != self.device:
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
+        stride = t.stride()
+        if n > 1 and stride[1] == d and stride[2] == 1:
+            return t.data_ptr(), stride[0]
         return t.data_ptr(), _context.token_stride(t)
 
     def _launch(self, fn: str, *args) -> None:
