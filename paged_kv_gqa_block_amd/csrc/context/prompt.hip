@@ -28,8 +28,8 @@
 // last rounding.
 //
 // Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 396-412 us
-// for 413 GFLOP, 1.04 PFLOP/s, 0.83-0.86 of what a square product of 8192 reaches on
-// the same card (over 4 bits: 385 us).  Matrix work fills half of a SIMD's cycles
+// for 413 GFLOP, 1.00-1.04 PFLOP/s, 0.83-0.86 of what a square product of 8192
+// reaches on the same card (over 4 bits: 385 us).  Matrix work fills half of a SIMD's cycles
 // and vector work (exponentials, maxima, rounding) 45 %, and the two hardly
 // overlap.  Direct loads and two scores in flight brought it from 502 us; deeper
 // rings of buffers, pages touched ahead in L2 (430 us), wave priorities and tiles
