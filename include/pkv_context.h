@@ -97,7 +97,8 @@ pkv_status pkv_kv4_load(const pkv_problem* prob, const int32_t* tok_offsets, int
  * pkv_attend_kv4 the 4-bit pool.  Only pages that hold a visible token are
  * read.  Each row's list of visible pages is cut into up to max_splits equal
  * ranges, max(1, ceil(T_max / max_splits)) pages each with T_max the longest
- * row's list.
+ * row's list, or more pages where the ranges then fill the compute units of the
+ * current device evenly.
  *   workspace: at least pkv_attend_workspace_bytes(prob, max_splits) bytes of
  *     device memory, 16-byte aligned, the first 256 KiB (one counter for each of
  *     65536 pairs of row and KV head) zero before the first call that uses it;

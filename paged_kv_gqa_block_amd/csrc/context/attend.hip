@@ -24,32 +24,103 @@
 // 96 rows x 8 heads x 8192 tokens in 4 bits took 190 us instead of 160.
 // Joining in the same launch: one row of 32768 tokens in 4 bits, 8 KV heads,
 // took 18.1 us with a second launch and 17.0 us so, and the host one call less
-// (16 -> 9 us).
+// (16 -> 9 us); with 16 states on their way at once 15.8 us.
 //
 // Measured (G = 8, d = 128, 64 rows, 8 KV heads, bf16): 4 bits, 1.1 million
-// tokens (1.21 GB): 234 us, 5.2 TB/s; the same pages read and not used take
+// tokens (1.21 GB): 212-223 us, 5.4-5.7 TB/s; the same pages read and not used take
 // 187 us (6.5 TB/s), the rest is conversion and matrix work that three waves do
-// not hide.  16 bits, window 1000 and 5 sinks (260 MB): 44 us, 5.9 TB/s; window
+// not hide (221 vector instructions for two pages).  Eight rows, half of them short
+// (111 MB): 28-29 us.  One row of 32768: 15.7-16 us.  16 bits, window 1000 and 5 sinks (260 MB): 44 us, 5.9 TB/s; window
 // 4096 over eight rows (134 MB): 27 us, 5.0 TB/s.  Small calls: 7 us, a chain of
 // dependent loads (length, page number, page, state, counter).
+#include <atomic>
+
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"
 #include "states.h"
+#include "wave.h"
 
 namespace pkv {
 namespace {
 
-// Pages of a split: the longest row's visible pages over the split cap.
-// Computed by every wave from the device lengths.
-__device__ __forceinline__ int split_pages(const AttendArgs& a) {
-  int t_max = 0;
-  for (int r = threadIdx.x & 63; r < a.batch; r += 64) {
-    const int n = clean_len(a.seq_lens[r], a.max_pages);
-    if (n > 0) t_max = max(t_max, seen_pages(n - 1, n - 1, a.window, a.sinks).count);
+// A workgroup's share of a row.
+struct Share {
+  int row;
+  int split;  // negative: no share
+  int pages;  // of every range but a row's last
+  int n;      // the row's length
+};
+
+// Share number `item` in the list of every row's ranges, row after row.  A range
+// has the longest row's visible pages over the split cap.  Workgroups without a
+// range come last in the launch: mixed in, as a grid of rows by splits has them,
+// they leave compute units short of real ones (64 rows of 1024 to 32768 tokens:
+// 600 resident workgroups of 768).
+__device__ __forceinline__ Share find_share(const AttendArgs& a, int item) {
+  Share s{item, 0, 0x7fffffff, 0};
+  if (a.splits == 1) {
+    s.n = clean_len(a.seq_lens[item], a.max_pages);
+    return s;
   }
-  t_max = __builtin_amdgcn_readfirstlane(wave_max_i(t_max));
-  return max(1, (t_max + a.splits - 1) / a.splits);
+  const int lane = threadIdx.x & 63;
+  int n, pages;
+  auto load = [&](int r0) {
+    const int r = r0 + lane;
+    n = r < a.batch ? clean_len(a.seq_lens[r], a.max_pages) : 0;
+    pages = n > 0 ? seen_pages(n - 1, n - 1, a.window, a.sinks).count : 0;
+  };
+  load(0);
+  int t_max = pages;
+  if (a.batch > 64) {
+    for (int r0 = 64; r0 < a.batch; r0 += 64) {
+      load(r0);
+      t_max = max(t_max, pages);
+    }
+    load(0);
+  }
+  t_max = wave_max(t_max);
+  s.pages = max(1, (t_max + a.splits - 1) / a.splits);
+  s.split = -1;
+  auto ranges = [&](int r0) {
+    return r0 + lane < a.batch ? max(1, (pages + s.pages - 1) / s.pages) : 0;
+  };
+  // A few workgroups for every compute unit, and some left over, take as long as
+  // one more for each: then longer ranges that come out even, where they cost less
+  // (a range is worth 8 pages more than it reads).  Eight rows, half of them short:
+  // 552 ranges 34 us, 512 ranges 28 us.
+  if (a.batch > 1 && a.batch <= 64) {
+    const int total = __builtin_amdgcn_readlane(wave_scan(ranges(0)), 63);
+    const int rounds = (total * a.num_kv_heads + a.cus - 1) / a.cus;
+    if (rounds >= 2 && rounds <= 4) {
+      const int even = (rounds - 1) * a.cus / a.num_kv_heads, first = s.pages;
+      int t = total;
+      for (int i = 0; i < 3 && t > even && even >= a.batch; ++i) {
+        s.pages += 1 + static_cast<int>(static_cast<float>(s.pages) *
+                                        static_cast<float>(t - even) / static_cast<float>(even));
+        s.pages = min(s.pages, t_max);
+        t = __builtin_amdgcn_readlane(wave_scan(ranges(0)), 63);
+      }
+      if (t > even || (rounds - 1) * (s.pages + 8) >= rounds * (first + 8)) s.pages = first;
+    }
+  }
+  for (int r0 = 0, before = 0;;) {
+    const int mine = ranges(r0);
+    const int upto = wave_scan(mine);
+    const int all = __builtin_amdgcn_readlane(upto, 63);
+    if (item < before + all) {
+      const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > item);
+      const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
+      s.row = r0 + at;
+      s.split = item - before - __builtin_amdgcn_readlane(upto - mine, at);
+      s.n = __builtin_amdgcn_readlane(n, at);
+      return s;
+    }
+    before += all;
+    r0 += 64;
+    if (r0 >= a.batch) return s;
+    load(r0);
+  }
 }
 
 // The loads of one page, as each format lays it out.
@@ -151,20 +222,20 @@ void attend_kernel(AttendArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, kg = lane >> 4;
-  const int g = blockIdx.x, split = blockIdx.y, row = blockIdx.z;
+  const int g = blockIdx.x;
+  const Share share = find_share(a, static_cast<int>(blockIdx.y + a.splits * blockIdx.z));
+  const int row = share.row, split = share.split, n = share.n;
   const int G = a.group, hkv = a.num_kv_heads;
-  const int n = clean_len(a.seq_lens[row], a.max_pages);
+  if (split < 0) return;
   if (n == 0) {  // an empty row sees nothing
-    if (split == 0) {
-      const int64_t h0 = int64_t(row) * a.num_q_heads + g * G;
-      for (int e = threadIdx.x; e < G * D; e += NW * 64)
-        static_cast<uint16_t*>(a.out)[h0 * D + e] = 0;
-      if (a.lse && threadIdx.x < G) a.lse[h0 + threadIdx.x] = kNegInf;
-    }
+    const int64_t h0 = int64_t(row) * a.num_q_heads + g * G;
+    for (int e = threadIdx.x; e < G * D; e += NW * 64)
+      static_cast<uint16_t*>(a.out)[h0 * D + e] = 0;
+    if (a.lse && threadIdx.x < G) a.lse[h0 + threadIdx.x] = kNegInf;
     return;
   }
   const SeenPages sp = seen_pages(n - 1, n - 1, a.window, a.sinks);
-  const int pps = a.splits > 1 ? split_pages(a) : sp.count;
+  const int pps = min(share.pages, sp.count);
   const int pb = split * pps;
   const int pe = min(pb + pps, sp.count);
   if (pb >= pe) return;
@@ -401,7 +472,7 @@ void attend_kernel(AttendArgs a) {
     if (whole) {
       write_out<D, BF16>(a, int64_t(row) * a.num_q_heads + g * G + h, c4, mx, l, o);
     } else {
-      put_state(a.st_o + (slot * G + h) * D + 4 * c4, o);
+      put_state4<D>(a.st_o + (slot * G + h) * D, c4, o);
       if (c4 == 0) put_state(a.st_ml + (slot * G + h) * 2, mx, l);
     }
   }
@@ -411,7 +482,7 @@ void attend_kernel(AttendArgs a) {
   // Its sum runs in split order, so the result does not depend on who arrives
   // last.  M = max m_s, w_s = 2^(m_s - M), out = sum w_s o_s / sum w_s l_s.
   const int ns = (sp.count + pps - 1) / pps;
-  if (!last_to_arrive(a.arrivals + pair, ns, &s_last)) return;
+  if (!last_to_arrive(arrival_counter(a.arrivals, pair), ns, &s_last)) return;
   // Threads take (head, chunk of four channels) and, where there are more
   // threads than that, a share of the splits each.
   const int items = G * C4;
@@ -426,20 +497,22 @@ void attend_kernel(AttendArgs a) {
     float m = kLowest, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
-      constexpr int U = 8;  // states in flight
-      for (int s0 = sg; s0 < ns; s0 += sg_n * U) {
+      constexpr int U = 16;  // states in flight
+      for (int s0 = 0; s0 < ns; s0 += sg_n * U) {
         float2 ml[U];
         float4 os[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int s = min(s0 + u * sg_n, ns - 1);
+          if (s0 + u * sg_n >= ns) break;  // for every share
+          const int s = min(s0 + u * sg_n + sg, ns - 1);
           const int64_t at = (first + s) * G + h;
           ml[u] = get_state2(a.st_ml + at * 2);
-          os[u] = get_state4(a.st_o + at * D + 4 * c4);
+          os[u] = get_state4<D>(a.st_o + at * D, c4);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (s0 + u * sg_n < ns) join(m, l, o, ml[u].x, ml[u].y, os[u]);
+          if (s0 + u * sg_n >= ns) break;
+          if (s0 + u * sg_n + sg < ns) join(m, l, o, ml[u].x, ml[u].y, os[u]);
         }
       }
     }
@@ -484,8 +557,21 @@ void launch_fmt(bool kv4, const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& a, hipStream_t s) {
+int current_compute_units() {
+  static std::atomic<int> known[64];
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  if (dev < 64 && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return 0;
+  if (dev < 64) known[dev].store(cus, std::memory_order_relaxed);
+  return cus;
+}
+
+pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& args, hipStream_t s) {
   const bool bf = p.dtype == PKV_BF16;
+  AttendArgs a = args;
+  if (a.splits > 1 && (a.cus = current_compute_units()) <= 0) return PKV_EHIP;
   if (p.head_dim == 128) {
     if (bf) launch_fmt<128, true>(kv4, a, s);
     else launch_fmt<128, false>(kv4, a, s);

@@ -282,15 +282,20 @@ extern "C" int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* vi
   const int64_t pairs = int64_t(prob->batch) * prob->num_kv_heads;
   const int64_t pages = most_pages(prob, view);
   // One range for every compute unit, as long as a range keeps eight pages (one
-  // unit for each wave); beyond that ranges of at least 96 pages, up to twelve
-  // a compute unit, so that rows of different lengths even out.  Joining costs
-  // more than it gives where ranges are shorter: 64 pairs of 2048 pages took
-  // 51 us in 4, 34 us in 16 and 38 us in 32 ranges each.
+  // unit for each wave); beyond that ranges of at least 96 pages, up to twenty
+  // a compute unit, so that rows of different lengths even out (the launch takes
+  // fewer where that comes out even).  Joining costs more than it gives where
+  // ranges are shorter: 512 pairs of 64 to 2048 pages took 237 us in up to 4, 222 in
+  // 6, 212 in 10 and 231 in 24 ranges each.  Eight pairs a compute unit come out even
+  // whole: 1024 pairs of up to 1024 pages 235 us whole and 219 in 3 to 5 ranges, 2048
+  // of up to 512 222 and 222, 4096 of up to 256 213 and 253 in 2.
   // Up to 40 pages stay whole: joining waits for stores, a counter and loads, 3 us.
   // One row, 8 heads, in one range and in as many as fill: 24 pages 6.0 and 7.5 us,
   // 40 pages 7.8 and 7.7 (16 bits: 6.3 and 7.4, 8.4 and 7.6), 64 pages 10.3 and 7.9.
   const int64_t fill = pages <= 40 ? 1 : std::min(ceil_div(num_cus, pairs), ceil_div(pages, 8));
-  const int64_t even = std::min(pages / 96, int64_t(12) * num_cus / pairs);
+  const int64_t even = pairs >= 8 * int64_t(num_cus)
+                           ? 1
+                           : std::min(pages / 96, 20 * int64_t(num_cus) / pairs);
   return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::max(fill, even), 1024)));
 }
 

@@ -46,6 +46,7 @@ struct AttendArgs {
   const void* v_pool;
   const int32_t* block_table;
   const int32_t* seq_lens;
+  int32_t cus;          // compute units of the device, set by the launcher
   float* st_ml;         // [slots][G][2]: running max (log2 units) and sum
   float* st_o;          // [slots][G][d]
   int32_t* arrivals;    // [B * Hkv], zero between calls
@@ -143,6 +144,9 @@ inline size_t prompt_state_floats(int head_dim) { return 256 * (size_t(head_dim)
 inline int64_t prompt_tiles(const PromptArgs& a) {
   return a.tok_offsets ? tile_base(a.num_tokens, a.batch, a.group) : int64_t(a.batch);
 }
+
+// Compute units of the current device; 0 where the query fails.
+int current_compute_units();
 
 pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& a, hipStream_t s);
 pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hipStream_t s);

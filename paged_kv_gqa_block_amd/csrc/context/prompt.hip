@@ -447,7 +447,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
       for (int i = 0; i < 8; ++i)
         put_state(mine_st + ((cb * 8 + i) * 256 + tid) * 2, acc[cb][2 * i], acc[cb][2 * i + 1]);
     put_state(mine_st + (NC * 8 * 256 + tid) * 2, m_run, l);
-    if (!last_to_arrive(a.arrivals + tg, ns, &s_last)) return;
+    if (!last_to_arrive(arrival_counter(a.arrivals, tg), ns, &s_last)) return;
     // Joined in split order, so that the result does not depend on the order
     // of arrival: first the maximum, then the weighted sums.
     const float* st0 = a.state + tg * a.splits * kSlot;
@@ -517,10 +517,8 @@ pkv_status launch_prompt(const pkv_problem& p, bool kv4, const PromptArgs& a, hi
   // Workgroups a KV head that run at the same time: two a compute unit.
   int slots = 0;
   if (a.splits > 1) {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-      return PKV_EHIP;
+    const int cus = current_compute_units();
+    if (cus <= 0) return PKV_EHIP;
     slots = 2 * cus / a.num_kv_heads;
   }
   if (p.head_dim == 128) {

@@ -3,6 +3,7 @@
 
 #include "context_internal.h"
 #include "mfma.h"
+#include "wave.h"
 
 namespace pkv {
 
@@ -57,17 +58,6 @@ __device__ __forceinline__ Run find_run(const Args& a, int64_t item, Base base) 
 template <typename Args>
 __device__ __forceinline__ Run single_run(const Args& a, int row) {
   return make_run(row, row, row + 1, a.seq_lens[row], a.max_pages);
-}
-
-// Inclusive sum over the wave's lanes.
-__device__ __forceinline__ int wave_scan(int x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int sh = 1; sh < 64; sh <<= 1) {
-    const int y = __builtin_amdgcn_ds_bpermute(((lane - sh) & 63) << 2, x);
-    x += lane >= sh ? y : 0;
-  }
-  return x;
 }
 
 // Query tiles of a prompt: row after row, the late tiles of a row first.
