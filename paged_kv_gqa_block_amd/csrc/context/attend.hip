@@ -497,7 +497,7 @@ void attend_kernel(AttendArgs a) {
     float m = kLowest, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
-      constexpr int U = 16;  // states in flight
+      constexpr int U = D / 8;  // states in flight (d = 64: four shares, so fewer each)
       for (int s0 = 0; s0 < ns; s0 += sg_n * U) {
         float2 ml[U];
         float4 os[U];
