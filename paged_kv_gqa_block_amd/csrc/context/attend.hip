@@ -27,12 +27,13 @@
 // (16 -> 9 us); with 16 states on their way at once 15.8 us.
 //
 // Measured (G = 8, d = 128, 64 rows, 8 KV heads, bf16): 4 bits, 1.1 million
-// tokens (1.21 GB): 212-223 us, 5.4-5.7 TB/s; the same pages read and not used take
+// tokens (1.21 GB): 212-227 us, 5.3-5.7 TB/s; the same pages read and not used take
 // 187 us (6.5 TB/s), the rest is conversion and matrix work that three waves do
-// not hide (221 vector instructions for two pages).  Eight rows, half of them short
-// (111 MB): 28-29 us.  One row of 32768: 15.7-16 us.  16 bits, window 1000 and 5 sinks (260 MB): 44 us, 5.9 TB/s; window
-// 4096 over eight rows (134 MB): 27 us, 5.0 TB/s.  Small calls: 7 us, a chain of
-// dependent loads (length, page number, page, state, counter).
+// not hide (221 vector instructions for two pages).  Eight rows, half of them
+// short (111 MB): 28-29 us.  One row of 32768: 15-16 us.  16 bits, window 1000 and
+// 5 sinks (260 MB): 44 us, 5.9 TB/s; window 4096 over eight rows (134 MB): 27 us,
+// 5.0 TB/s.  Small calls: 7 us, a chain of dependent loads (length, page number,
+// page, state, counter).
 #include <atomic>
 
 #include "context_internal.h"
