@@ -78,12 +78,12 @@ __device__ __forceinline__ float sum_x32(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Largest of three, one instruction: fmaxf of matrix-core results would first
-// quieten each operand.  A NaN loses against a number, as with fmaxf.
+// Largest of three, one instruction (v_maximum3_f32): fmaxf of matrix-core results
+// would first quieten each operand.  A NaN wins.  Left to the compiler, which keeps
+// the wait that a vector read of a matrix-core result needs; it knows of none in
+// front of inline asm.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // Where a running maximum starts: finite, so that a score of -inf weighs
