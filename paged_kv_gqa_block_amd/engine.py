@@ -177,10 +177,28 @@ class SelfPlannedStep(_PersistentStepBuffers):
         return self.out, self.lse
 
 
+def _await_buffers(device: torch.device) -> None:
+    """Wait until new buffers of `device` are ready: their zeros were filled, and
+    earlier owners of their memory were done, in the order of the current stream
+    alone, and a step may run on any.  Not inside a graph capture, where the
+    fills become part of the graph."""
+    if device.type == "cuda":
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
+
 class _ContextCalls:
     """Argument checks and stream choice shared by the context operators
     (include/pkv_context.h).  They run on the device of their buffers, on the
-    given stream or that device's current one."""
+    given stream or that device's current one.
+
+    What an object allocates is ready when its constructor returns, for every
+    stream.  Its memory is not reused before work on a torch stream that it was
+    given is done; a stream given as a number is not torch's to wait for, so
+    keep the object until that work is done.  The caller's buffers have to be
+    ready on the stream of a call, and live until its work is done (until the
+    last call of a bound form), as with every torch call."""
 
     def __init__(self, prob: _lib.pkv_problem, device):
         self.prob = prob
@@ -199,11 +217,25 @@ class _ContextCalls:
                         "token": (p.num_kv_heads, p.head_dim),
                         "q": (p.batch, p.num_q_heads, p.head_dim)}
         self._prob_ref = ctypes.byref(prob)
+        self._buffers, self._streams = (), set()
+
+    def _own_buffers(self, *buffers: torch.Tensor) -> None:
+        """Take charge of buffers just allocated on the current stream."""
+        _await_buffers(self.device)
+        self._buffers = buffers
+        self._streams = {torch._C._cuda_getCurrentRawStream(self._index)}
 
     def _stream(self, stream) -> int:
-        if stream is not None:
-            return stream if isinstance(stream, int) else stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is None:
+            handle = torch._C._cuda_getCurrentRawStream(self._index)
+        else:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle not in self._streams and not isinstance(stream, int):
+            at = torch.cuda.current_stream(self.device) if stream is None else stream
+            for t in self._buffers:
+                t.record_stream(at)
+            self._streams.add(handle)
+        return handle
 
     def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
         """The address of `t`, after its checks."""
@@ -270,11 +302,14 @@ class Kv4Cache(_ContextCalls):
 
     def __init__(self, prob: _lib.pkv_problem, pool: torch.Tensor | None = None, device="cuda"):
         super().__init__(prob, pool.device if pool is not None else device)
-        if pool is None:
+        own = pool is None
+        if own:
             pool = torch.zeros(prob.num_pool_pages, prob.num_kv_heads, self.kv4_page_bytes,
                                dtype=torch.uint8, device=self.device)
         self._kv4_pool(pool)
         self.pool = pool
+        if own:
+            self._own_buffers(pool)
 
     def store(self, k_new, v_new, block_table, seq_lens, tok_offsets=None, stream=None) -> None:
         """k_new, v_new: [tokens][Hkv][d], heads contiguous, any token stride
@@ -338,6 +373,7 @@ class WindowStep(_ContextCalls):
                                device=self.device)
         self.lse = torch.empty(prob.batch, prob.num_q_heads, dtype=torch.float32,
                                device=self.device)
+        self._own_buffers(self.workspace, self.out, self.lse)
         self._view_ref = ctypes.byref(self.view)
         self._own = (self.workspace.data_ptr(), nbytes, self.out.data_ptr(), self.lse.data_ptr())
 
@@ -393,6 +429,7 @@ class PromptStep(_ContextCalls):
                                device=self.device)
         self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
                                device=self.device)
+        self._own_buffers(self.workspace, self.out, self.lse)
         self._view_ref = ctypes.byref(self.view)
         self._own = (self.workspace.data_ptr(), nbytes, self.out.data_ptr(), self.lse.data_ptr())
 

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from paged_kv_gqa_block_amd import engine
-from tests.context_cases import Batch
+from tests.context_cases import Batch, check
 from tests.parity import say
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,119 @@ def test_non_finite_seen_token_stays_in_its_row(value, kv4, dtype):
             else q[..., 3].float() * value > 0
         assert torch.equal(torch.isnan(hit).all(-1), want)
         assert torch.equal(torch.isfinite(hit).all(-1), ~want)
+
+
+# ---- streams -----------------------------------------------------------------------------
+
+def _busy(stream, ms=60):
+    """Keep `stream` at work for a while: passes over 1 GiB of its own."""
+    with torch.cuda.stream(stream):
+        x = torch.zeros(1 << 28, dtype=torch.float32, device="cuda")
+        for _ in range(2 * ms):
+            x.add_(1)
+
+
+def _litter(nbytes):
+    """Leave set bits in the memory that the current stream's next buffers of
+    these sizes get."""
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in nbytes]
+    del junk
+
+
+KINDS = ["window", "kv4", "prompt"]
+
+
+def _of_kind(kind):
+    b = Batch(51, [900, 450, 77], [1, 1, 1] if kind != "prompt" else [3, 40, 77], hkv=2, group=4,
+              kv4=kind == "kv4")
+
+    def make():
+        if kind == "prompt":
+            return engine.PromptStep(b.problem(), int(b.new.sum()), splits=8)
+        return _step(b, 16)
+    return b, b.device(), make
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_step_built_on_a_busy_stream_runs_on_another(kind):
+    """The workspace's counters are zero and its memory free when the constructor
+    returns, whatever still runs on the stream that it was built on."""
+    b, w, make = _of_kind(kind)
+    sizes = [t.numel() * t.element_size() for t in (lambda s: (s.workspace, s.out, s.lse))(make())]
+    building, running = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say(f"[built elsewhere] {kind}")
+    with torch.cuda.stream(building):
+        _litter(sizes)
+        _busy(building)
+        step = make()
+    out, lse = step.run(w, running)
+    running.synchronize()
+    check(out, lse, b.reference(), "f16", 128, b.vmax, kind == "prompt", kind)
+    torch.cuda.synchronize()
+    assert not step.workspace[:256 << 10].any()
+
+
+@pytest.mark.parametrize("given", ["argument", "current"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_dropped_step_keeps_its_memory_until_its_stream_is_done(kind, given):
+    """A step that is dropped while its call waits on another stream: the memory
+    of its workspace goes to nobody else before the call is done."""
+    b, w, make = _of_kind(kind)
+    running = torch.cuda.Stream()
+    step = make()
+    at, size = step.workspace.data_ptr(), step.workspace.numel()
+    torch.cuda.synchronize()
+    say(f"[dropped] {kind} {given}")
+    _busy(running)
+    if given == "argument":
+        out, lse = step.run(w, running)
+    else:
+        with torch.cuda.stream(running):
+            out, lse = step.run(w)
+    del step
+    other = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert all(t.data_ptr() != at for t in other)
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "f16", 128, b.vmax, kind == "prompt", kind)
+
+
+def test_new_cache_built_on_a_busy_stream_keeps_what_another_stores():
+    """The zeros of a new 4-bit pool are there before anything is stored."""
+    b = Batch(52, [100, 40], [100, 40], hkv=2, group=1, kv4=True)
+    w, n = b.device(), 140
+    x = torch.randn(n, 2, 128, generator=torch.Generator().manual_seed(1)).half().cuda()
+    outs = []
+    building, running = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say("[new cache]")
+    for _ in range(2):
+        with torch.cuda.stream(building):
+            _busy(building)
+            cache = engine.Kv4Cache(b.problem())
+        args = (w["block_table"], w["seq_lens"], w["tok_offsets"])
+        cache.store(x, x, *args, stream=running)
+        running.synchronize()
+        building.synchronize()
+        outs.append(cache.load(*args, torch.empty_like(x), torch.empty_like(x)))
+    torch.cuda.synchronize()
+    assert all(_same(a, c) for a, c in zip(*outs)) and outs[0][0].abs().sum() > 0
+    assert _same(outs[0][0], outs[0][1])
+
+
+def test_step_built_inside_a_capture():
+    """A step whose buffers and zeros belong to the graph: every replay is right."""
+    b, w, make = _of_kind("window")
+    want = [t.clone() for t in make().run(w)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step = make()
+        step.run(w)
+    for i in range(3):
+        say(f"[built in a capture] replay {i}")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert _same(step.out, want[0]) and _same(step.lse, want[1])
+        make().run(w)
+        torch.cuda.synchronize()
