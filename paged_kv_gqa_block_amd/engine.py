@@ -40,6 +40,17 @@ def to_device(w: dict, device="cuda") -> dict:
     return out
 
 
+def _await_buffers(device: torch.device) -> None:
+    """Wait until new buffers of `device` are ready: their zeros were filled, and
+    earlier owners of their memory were done, in the order of the current stream
+    alone, and a step may run on any.  Not inside a graph capture, where the
+    fills become part of the graph."""
+    if device.type == "cuda":
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
+
 class DecodeStep:
     """Buffers and calls for one (problem, path, split cap)."""
 
@@ -66,6 +77,7 @@ class DecodeStep:
         self.st_m = torch.empty(max(slots, 1), g, dtype=torch.float32, device=self.device)
         self.st_l = torch.empty(max(slots, 1), g, dtype=torch.float32, device=self.device)
         self.st_o = torch.empty(max(slots, 1), g, d, dtype=torch.float32, device=self.device)
+        _await_buffers(self.device)
 
     def plan(self, seq_lens_host: np.ndarray, stream=None) -> _lib.pkv_plan_info:
         self.info = pkv_plan(self.prob, np.ascontiguousarray(seq_lens_host, dtype=np.int32),
@@ -143,6 +155,7 @@ class DeviceStep(_PersistentStepBuffers):
             raise _lib.PkvError("pkv_plan_bytes", _lib.PKV_EINVAL, "invalid problem")
         self.plan_dev = torch.zeros(nbytes // 4, dtype=torch.int32, device=self.device)
         self.bad_rows = torch.zeros(1, dtype=torch.int32, device=self.device)
+        _await_buffers(self.device)
 
     def run(self, w: dict, stream=None):
         pkv_plan_device(self.prob, w["seq_lens"], self.splits, self.plan_dev,
@@ -167,6 +180,7 @@ class SelfPlannedStep(_PersistentStepBuffers):
     def __init__(self, prob: _lib.pkv_problem, splits: int, device="cuda"):
         super().__init__(prob, splits, device)
         self.counter = torch.zeros(1, dtype=torch.int32, device=self.device)
+        _await_buffers(self.device)
 
     def run(self, w: dict, stream=None):
         _lib.pkv_decode_selfplan(self.prob, w["seq_lens"], self.splits, self.counter, w["q"],
@@ -175,17 +189,6 @@ class SelfPlannedStep(_PersistentStepBuffers):
         _lib.pkv_merge_selfplan(self.prob, w["seq_lens"], self.splits, self.counter, self.st_m,
                                 self.st_l, self.st_o, self.out, self.lse, stream=stream)
         return self.out, self.lse
-
-
-def _await_buffers(device: torch.device) -> None:
-    """Wait until new buffers of `device` are ready: their zeros were filled, and
-    earlier owners of their memory were done, in the order of the current stream
-    alone, and a step may run on any.  Not inside a graph capture, where the
-    fills become part of the graph."""
-    if device.type == "cuda":
-        with torch.cuda.device(device):
-            if not torch.cuda.is_current_stream_capturing():
-                torch.cuda.current_stream().synchronize()
 
 
 class _ContextCalls:

@@ -113,6 +113,36 @@ def test_step_built_on_a_busy_stream_runs_on_another(kind):
     assert not step.workspace[:256 << 10].any()
 
 
+@pytest.mark.parametrize("kind", ["plan", "device", "selfplan"])
+def test_engine_step_built_on_a_busy_stream_runs_on_another(kind):
+    """The same of the steps over the whole context: plan, device plan and claim
+    counter are not cleared behind a call."""
+    b = Batch(53, [900, 450, 77], hkv=2, group=4)
+    w, host = b.device(), b.lens.copy()
+
+    def make():
+        if kind == "plan":
+            return engine.DecodeStep(b.problem(), "workqueue", 8)
+        return {"device": engine.DeviceStep, "selfplan": engine.SelfPlannedStep}[kind](b.problem(), 8)
+    first = make()
+    zeros = {"plan": "plan_dev", "device": "plan_dev", "selfplan": "counter"}[kind]
+    sizes = [t.numel() * t.element_size() for t in
+             (first.out, first.lse, first.st_m, first.st_l, first.st_o, getattr(first, zeros))]
+    building, running = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say(f"[engine step built elsewhere] {kind}")
+    with torch.cuda.stream(building):
+        _litter(sizes)
+        _busy(building)
+        step = make()
+    with torch.cuda.stream(running):
+        if kind == "plan":
+            step.plan(host, running)
+        step.run(w, running)
+    running.synchronize()
+    check(step.out, step.lse, b.reference(), "f16", 128, b.vmax, True, kind)
+
+
 @pytest.mark.parametrize("given", ["argument", "current"])
 @pytest.mark.parametrize("kind", KINDS)
 def test_dropped_step_keeps_its_memory_until_its_stream_is_done(kind, given):
