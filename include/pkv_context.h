@@ -26,6 +26,8 @@
  * a row sees may hold anything, NaN and infinities included; a NaN or an
  * infinity in a token that one query of a row sees may also reach other queries
  * of that row (never other rows).
+ * Scores, scale <q, k>, are held in fp32 and have to stay below 2^23 in magnitude,
+ * where neighbouring numbers are still 1/2 apart.
  *
  * 4-bit cache (kv4).  K and V share one pool, bytes
  *     kv4_pool [num_pool_pages][Hkv][17 d],

@@ -16,10 +16,10 @@
 //    stored in operand order and needs none.
 //  * P V: A = P (heads x tokens) from the lane's own scores, B = V (tokens x
 //    channels) by byte permutes.  P is split into its 16-bit rounding and the
-//    rounding of the rest, so the product keeps 16 (bf16) to 22 (f16) bits.
+//    rounding of the rest, so the product keeps 16 bits of a weight in bf16, and
+//    22 in f16 as far down as kDecodeReach says.
 //  * The running maximum only moves, and O is only rescaled, when a score passes
-//    it by more than 2^8 (kSlack): below that the weights stay exact enough in
-//    fp32 and fit in f16.
+//    it by a good deal (kDecodeReach).
 // Three waves of a SIMD (at most 168 registers): with the compiler's own two,
 // 96 rows x 8 heads x 8192 tokens in 4 bits took 190 us instead of 160.
 // Joining in the same launch: one row of 32768 tokens in 4 bits, 8 KV heads,
@@ -218,6 +218,7 @@ void attend_kernel(AttendArgs a) {
   constexpr int UP = KV4 ? 2 : 1;  // pages per unit
   constexpr int VEC = D / 16;      // channels per lane
   constexpr int NT = D / 32;       // score products per page
+  constexpr Reach kReach = kDecodeReach<BF16>;
   __shared__ AttendShared<D, GP, NW> sh;
   __shared__ bool s_last;
   const int lane = threadIdx.x & 63;
@@ -360,8 +361,8 @@ void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int i = 1; i < 4 * UP; ++i) top = fmaxf(top, xs[i]);
     top *= a.scale_log2;
-    if (__builtin_amdgcn_ballot_w64(top > m_run + kSlack) != 0) {  // rescale O and l
-      const float mn = fmaxf(m_run, max_x32(max_x16(top)));
+    if (__builtin_amdgcn_ballot_w64(top > m_run + (kReach.room + kReach.slack)) != 0) {  // rescale O and l
+      const float mn = fmaxf(m_run, max_x32(max_x16(top)) - kReach.room);
       const float alpha = fast_exp2(m_run - mn);
       l_part *= alpha;
 #pragma unroll

@@ -90,8 +90,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // exp2(-inf) = 0 and never meets -inf - -inf.
 constexpr float kLowest = -3.402823466e38f;
 
-// log2 of the largest weight that is kept without moving the running maximum.
-constexpr float kSlack = 8.f;
+// The running maximum that weights are relative to is kept `room` (log2) below
+// the largest score, and only moves when a score passes it by more than room +
+// slack: a weight is at most 2^(room + slack), and the largest at least 2^room.
+// An f16 weight below 2^-14 is subnormal, held to 2^-25, so its type needs room,
+// with 2^15 at the top; bf16 has the range of fp32 and needs none.
+//  * One part a weight (prompts): room 7 keeps the 11 bits of a weight down to
+//    2^-21 of the largest, and an error of 2^-32 of it below.
+//  * Two parts (decode): room 12 keeps 22 bits down to 2^-15 of the largest, 11
+//    down to 2^-26, and an error of 2^-37 of it below.  (With room 0, 1500
+//    tokens 17.4 nats under a first one whose V is zero gave an output 6 % off.)
+struct Reach {
+  float room, slack;
+};
+template <bool BF16>
+inline constexpr Reach kPromptReach = BF16 ? Reach{0.f, 8.f} : Reach{7.f, 8.f};
+template <bool BF16>
+inline constexpr Reach kDecodeReach = BF16 ? Reach{0.f, 8.f} : Reach{12.f, 3.f};
 
 // A row's length as the operators take it: 0 outside [0, capacity].
 __device__ __forceinline__ int clean_len(int n, int max_pages) {

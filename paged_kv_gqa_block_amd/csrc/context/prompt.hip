@@ -20,8 +20,8 @@
 //    matrix core works while the vector unit does.
 //  * 16-bit pages go to LDS directly (buffer_load ... lds); wave w brings page w
 //    of the step.
-//  * O is rescaled only when a score passes the running maximum by more than
-//    2^8 (kSlack).
+//  * O is rescaled only when a score passes the running maximum by a good deal
+//    (kPromptReach).
 // The probabilities enter the second product rounded to the problem's type (a
 // relative 2^-8 (bf16) or 2^-11 (f16) at most each, of the size of the output's
 // own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
@@ -272,9 +272,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   // This wave's loads have reached LDS.
   auto landed = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
 
-  // The running maximum is kept this far (log2) below the largest score: an f16
-  // weight of up to 2^15 then stays normal down to 2^-21 of the largest.
-  constexpr float kRoom = BF16 ? 0.f : 7.f;
+  constexpr Reach kReach = kPromptReach<BF16>;
 
   // ---- one step ---------------------------------------------------------------------
   float m_run = kLowest, l_part = 0.f;
@@ -326,8 +324,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
       t1 = max3(t1, s[0][i + 1], s[1][i + 1]);
     }
     const float top = max_x32(fmaxf(t0, t1)) * a.scale_log2;
-    if (__builtin_amdgcn_ballot_w64(top > m_run + kRoom + kSlack) != 0) {
-      const float mn = fmaxf(m_run, top - kRoom);
+    if (__builtin_amdgcn_ballot_w64(top > m_run + (kReach.room + kReach.slack)) != 0) {
+      const float mn = fmaxf(m_run, top - kReach.room);
       const float alpha = fast_exp2(m_run - mn);
       l_part *= alpha;
 #pragma unroll

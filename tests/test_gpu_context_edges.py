@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import context as oc
 from paged_kv_gqa_block_amd import engine
-from tests.context_cases import Batch, check
+from tests.context_cases import TORCH, Batch, check, f64, lse_bound, out_bound
 from tests.parity import say
 
 pytestmark = pytest.mark.gpu
@@ -206,3 +207,94 @@ def test_step_built_inside_a_capture():
         assert _same(step.out, want[0]) and _same(step.lse, want[1])
         make().run(w)
         torch.cuda.synchronize()
+
+
+# ---- weights far apart --------------------------------------------------------------------
+
+def _one_row(q, k, v, scale, kv4, dtype):
+    """A row of n tokens stored through the framework: (problem, call arguments,
+    K and V as the cache holds them in fp64).  q [m][Hq][d] are its last m tokens."""
+    n, hkv, d = k.shape
+    pages = -(-n // 16)
+    prob = engine.make_problem(1, q.shape[1], hkv, d, 16, pages, pages, dtype, scale)
+    w = {"q": q.cuda(), "block_table": torch.randperm(
+            pages, generator=torch.Generator().manual_seed(n)).int().view(1, -1).cuda(),
+         "seq_lens": torch.tensor([n], dtype=torch.int32).cuda()}
+    off = torch.tensor([0, n], dtype=torch.int32).cuda()
+    if kv4:
+        cache = engine.Kv4Cache(prob)
+        cache.store(k.cuda(), v.cuda(), w["block_table"], w["seq_lens"], off)
+        w["kv4_pool"] = cache.pool
+        k, v = (oc.kv4_values(*oc.kv4_quantise(f64(x), dtype)) for x in (k, v))
+    else:
+        w["k_pool"], w["v_pool"] = (torch.zeros(pages, hkv, 16, d, dtype=TORCH[dtype],
+                                                device="cuda") for _ in range(2))
+        engine.store_kv(prob, k.cuda(), v.cuda(), w["block_table"], w["seq_lens"], off,
+                        w["k_pool"], w["v_pool"])
+        k, v = f64(k), f64(v)
+    return prob, w, k, v
+
+
+def _within(out, lse, ref, dtype, d, vmax, one_part, label):
+    """The element bounds of tests/context_cases.py with the kernels' own share of
+    f16 weights that are subnormal: the largest weight of a query is kept at 2^7
+    or more (prompt) or 2^12 or more (decode), so a part of one is off by at most
+    2^-25 / 2^7 or 2^-25 / 2^12 of the largest, n times."""
+    want, want_lse, (mag, score_mag, count) = ref
+    bound = out_bound(want, mag, score_mag, count, 0.0, d, dtype, one_part)
+    if dtype == "f16":
+        bound = bound + count.reshape(-1, 1, 1) * 2.0 ** (-32 if one_part else -37) * vmax
+    over = np.abs(f64(out) - want) / bound
+    assert np.isfinite(f64(out)).all() and over.max() <= 1, f"{label}: {over.max():.2f} of the bound"
+    lo = np.abs(f64(lse) - want_lse) / lse_bound(want_lse, score_mag, count, d)
+    assert lo.max() <= 1, f"{label}: lse {lo.max():.2f} of the bound"
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("d,dtype", [(128, "f16"), (64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("gap", [6, 10, 14, 16, 17.4, 20, 24])
+def test_one_token_far_above_the_rest(gap, d, dtype, kv4, many):
+    """A first token whose weight exceeds each other's by exp(gap) and whose V is
+    zero, as a sink's often is: the output is what the others leave."""
+    say(f"[sink] gap={gap} d={d} {dtype} kv4={kv4} prompt={many}")
+    rng = np.random.default_rng(int(10 * gap))
+    n, hkv, group = 1500, 2, 4
+    t = TORCH[dtype]
+    q = torch.zeros(5 if many else 1, hkv * group, d)
+    q[..., 0] = 8.0
+    q[..., 32:] = torch.from_numpy(rng.standard_normal((*q.shape[:2], d - 32)).astype(np.float32))
+    k = torch.from_numpy(rng.standard_normal((n, hkv, d)).astype(np.float32)) * 0.05
+    k[..., 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = 3.0  # exact in 4 bits
+    v = 50 + 50 * torch.from_numpy(rng.standard_normal((n, hkv, d)).astype(np.float32))
+    v[0] = 0.0
+    scale = float(np.float32(gap / 24.0))
+    prob, w, k64, v64 = _one_row(q.to(t), k.to(t), v.to(t), scale, kv4, dtype)
+    m = q.shape[0]
+    ref = oc.attend_row(f64(q.to(t)), range(n - m, n), k64, v64, scale)
+    if many:
+        w["tok_offsets"] = torch.tensor([0, m], dtype=torch.int32).cuda()
+        steps = [engine.PromptStep(prob, m, splits=s) for s in (1, 4)]
+    else:
+        steps = [(engine.Kv4Step if kv4 else engine.WindowStep)(prob, splits=s) for s in (1, 5)]
+    for step in steps:
+        out, lse = step.run(w)
+        torch.cuda.synchronize()
+        _within(out, lse, ref, dtype, d, np.abs(v64).max(), many, f"splits {step.splits}")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale,spread", [(-0.2, 1.0), (0.0, 1.0), (1.0, 1.0), (1.0, 2.0),
+                                          (1e-30, 1.0)])
+def test_scales_of_every_type_and_kind(scale, spread, dtype, kv4, many):
+    say(f"[scales] {scale} spread={spread} {dtype} kv4={kv4} prompt={many}")
+    b = Batch(54, [90, 300, 40], [90, 20, 10] if many else None, scale=scale, spread=spread,
+              dtype=dtype, kv4=kv4)
+    step = engine.PromptStep(b.problem(), int(b.new.sum())) if many else _step(b)
+    out, lse = step.run(b.device())
+    torch.cuda.synchronize()
+    _within(out, lse, b.reference(), dtype, 128, b.vmax, many, f"scale {scale}")
