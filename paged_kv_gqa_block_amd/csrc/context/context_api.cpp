@@ -2,6 +2,7 @@
 // launches on the caller's stream.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "context_internal.h"
 #include "launch_limits.h"
@@ -28,12 +29,13 @@ int32_t clean_window(const pkv_problem* p, const pkv_view* view) {
 
 // The kernels take maxima of unscaled scores, so their scale is positive: the
 // sign of a negative one moves to the queries, and zero becomes the smallest
-// normal number, which gives every finite score a weight of exactly 1.
+// number there is, which takes every finite score to 5e-7 or less: a weight of 1
+// within fp32.  (The smallest normal number took scores of 2^125 to 1/2.)
 template <typename Args>
 void set_scale(const pkv_problem* p, Args* a) {
   const float x = p->sm_scale * kLog2e;
   a->q_flip = x < 0.f ? 0x80008000u : 0u;
-  a->scale_log2 = std::max(std::fabs(x), 1.17549435e-38f);
+  a->scale_log2 = std::max(std::fabs(x), std::numeric_limits<float>::denorm_min());
 }
 
 // Largest number of pages that one query of this problem sees.

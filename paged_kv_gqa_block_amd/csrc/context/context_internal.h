@@ -61,7 +61,7 @@ struct AttendArgs {
   int32_t splits;
   int32_t window;       // 0: everything
   int32_t sinks;
-  float scale_log2;     // |scale| log2(e), at least the smallest normal number
+  float scale_log2;     // |scale| log2(e), above zero (subnormal where need be)
   uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
 };
 
@@ -87,7 +87,7 @@ struct PromptArgs {
   int32_t splits;
   int32_t window;
   int32_t sinks;
-  float scale_log2;     // |scale| log2(e), at least the smallest normal number
+  float scale_log2;     // |scale| log2(e), above zero (subnormal where need be)
   uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
 };
 

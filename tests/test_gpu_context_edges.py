@@ -298,3 +298,19 @@ def test_scales_of_every_type_and_kind(scale, spread, dtype, kv4, many):
     out, lse = step.run(b.device())
     torch.cuda.synchronize()
     _within(out, lse, b.reference(), dtype, 128, b.vmax, many, f"scale {scale}")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-38, -1e-38, 1e-39])
+def test_smallest_scales_of_the_largest_products(scale, kv4, many):
+    """bf16 products <q, k> near 2^124: a scale of zero weighs every token alike, and
+    one about the smallest normal number keeps its value."""
+    say(f"[smallest scales] {scale} kv4={kv4} prompt={many}")
+    b = Batch(55, [90, 300, 40], [90, 20, 10] if many else None, scale=scale, spread=2.0 ** 60,
+              dtype="bf16", kv4=kv4)
+    b.q = b.q * 2.0 ** 60
+    step = engine.PromptStep(b.problem(), int(b.new.sum())) if many else _step(b)
+    out, lse = step.run(b.device())
+    torch.cuda.synchronize()
+    _within(out, lse, b.reference(), "bf16", 128, b.vmax, many, f"scale {scale}")
