@@ -98,9 +98,10 @@ pkv_status pkv_kv4_load(const pkv_problem* prob, const int32_t* tok_offsets, int
  * visible part of the cache: pkv_attend_window reads 16-bit pages,
  * pkv_attend_kv4 the 4-bit pool.  Only pages that hold a visible token are
  * read.  Each row's list of visible pages is cut into up to max_splits equal
- * ranges, max(1, ceil(T_max / max_splits)) pages each with T_max the longest
- * row's list, or more pages where the ranges then fill the compute units of the
- * current device evenly.
+ * ranges, ceil(T_max / s) pages each with T_max the longest row's list and s the
+ * least of max_splits and what pkv_attend_splits gives where a table holds T_max
+ * pages (so short rows under a wide table stay whole), or more pages where the
+ * ranges then fill the compute units of the current device evenly.
  *   workspace: at least pkv_attend_workspace_bytes(prob, max_splits) bytes of
  *     device memory, 16-byte aligned, the first 256 KiB (one counter for each of
  *     65536 pairs of row and KV head) zero before the first call that uses it;
@@ -144,10 +145,11 @@ int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* view, int32_t
  * P enters the second product rounded to the problem's type; statistics and
  * sums are held in fp32.
  *   max_splits: a tile of 128 query rows (tokens times heads of a group) cuts
- *     its keys into up to this many ranges, for few queries over long contexts,
- *     and no more than fill the current device with the tiles there are; 1 needs
- *     no workspace.  pkv_prompt_splits gives a cap that fills num_cus
- *     compute units (0 on an invalid argument).
+ *     its keys into up to this many ranges, for few queries over long contexts:
+ *     no more than fill the current device with the tiles there are, and of 512
+ *     keys or more each (a tile's last one aside); 1 needs no workspace.
+ *     pkv_prompt_splits gives a cap that fills num_cus compute units (0 on an
+ *     invalid argument).
  *   workspace: pkv_prompt_workspace_bytes device bytes (0 for one split and
  *     where the call would be refused), on the terms of pkv_attend_window's;
  *     one_per_row says that the call passes no tok_offsets.

@@ -54,7 +54,8 @@ struct Share {
 };
 
 // Share number `item` in the list of every row's ranges, row after row.  A range
-// has the longest row's visible pages over the split cap.  Workgroups without a
+// has the longest row's visible pages over the ranges that they are worth
+// (decode_ranges), the split cap at most.  Workgroups without a
 // range come last in the launch: mixed in, as a grid of rows by splits has them,
 // they leave compute units short of real ones (64 rows of 1024 to 32768 tokens:
 // 600 resident workgroups of 768).
@@ -81,7 +82,8 @@ __device__ __forceinline__ Share find_share(const AttendArgs& a, int item) {
     load(0);
   }
   t_max = wave_max(t_max);
-  s.pages = max(1, (t_max + a.splits - 1) / a.splits);
+  const int most = min(a.splits, decode_ranges(t_max, a.fill, a.even));
+  s.pages = max(1, (t_max + most - 1) / most);
   s.split = -1;
   auto ranges = [&](int r0) {
     return r0 + lane < a.batch ? max(1, (pages + s.pages - 1) / s.pages) : 0;
@@ -89,7 +91,8 @@ __device__ __forceinline__ Share find_share(const AttendArgs& a, int item) {
   // A few workgroups for every compute unit, and some left over, take as long as
   // one more for each: then longer ranges that come out even, where they cost less
   // (a range is worth 8 pages more than it reads).  Eight rows, half of them short:
-  // 552 ranges 34 us, 512 ranges 28 us.
+  // 552 ranges 34 us, 512 ranges 28 us.  (Counting again
+  // takes one scan where a wave holds the rows; more than 64 leave little over.)
   if (a.batch > 1 && a.batch <= 64) {
     const int total = __builtin_amdgcn_readlane(wave_scan(ranges(0)), 63);
     const int rounds = (total * a.num_kv_heads + a.cus - 1) / a.cus;
@@ -573,7 +576,10 @@ int current_compute_units() {
 pkv_status launch_attend(const pkv_problem& p, bool kv4, const AttendArgs& args, hipStream_t s) {
   const bool bf = p.dtype == PKV_BF16;
   AttendArgs a = args;
-  if (a.splits > 1 && (a.cus = current_compute_units()) <= 0) return PKV_EHIP;
+  if (a.splits > 1) {
+    if ((a.cus = current_compute_units()) <= 0) return PKV_EHIP;
+    ranges_of_device(int64_t(a.batch) * a.num_kv_heads, a.cus, &a.fill, &a.even);
+  }
   if (p.head_dim == 128) {
     if (bf) launch_fmt<128, true>(kv4, a, s);
     else launch_fmt<128, false>(kv4, a, s);

@@ -179,6 +179,9 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
   a.sinks = view ? view->sinks : 0;
   set_scale(prob, &a);
   a.splits = max_splits;
+  // Its first token's view, and a page more for every 16 tokens behind that.
+  a.tile_pages = static_cast<int32_t>(
+      std::min<int64_t>(most_pages(prob, view) + kTileRows / a.group / 16 + 2, a.max_pages));
   const int64_t tiles = prompt_tiles(a);
   if (!prompt_fits(prob, tiles, max_splits)) return PKV_ERANGE;
   if (max_splits > 1) {
@@ -281,24 +284,10 @@ extern "C" int32_t pkv_attend_splits(const pkv_problem* prob, const pkv_view* vi
                                      int32_t num_cus) {
   if (check_problem(prob) != PKV_OK || check_view(view) != PKV_OK) return 0;
   if (num_cus < 1 || num_cus > 1024) return 0;
-  const int64_t pairs = int64_t(prob->batch) * prob->num_kv_heads;
-  const int64_t pages = most_pages(prob, view);
-  // One range for every compute unit, as long as a range keeps eight pages (one
-  // unit for each wave); beyond that ranges of at least 96 pages, up to twenty
-  // a compute unit, so that rows of different lengths even out (the launch takes
-  // fewer where that comes out even).  Joining costs more than it gives where
-  // ranges are shorter: 512 pairs of 64 to 2048 pages took 237 us in up to 4, 222 in
-  // 6, 212 in 10 and 231 in 24 ranges each.  Eight pairs a compute unit come out even
-  // whole: 1024 pairs of up to 1024 pages 235 us whole and 219 in 3 to 5 ranges, 2048
-  // of up to 512 222 and 222, 4096 of up to 256 213 and 253 in 2.
-  // Up to 40 pages stay whole: joining waits for stores, a counter and loads, 3 us.
-  // One row, 8 heads, in one range and in as many as fill: 24 pages 6.0 and 7.5 us,
-  // 40 pages 7.8 and 7.7 (16 bits: 6.3 and 7.4, 8.4 and 7.6), 64 pages 10.3 and 7.9.
-  const int64_t fill = pages <= 40 ? 1 : std::min(ceil_div(num_cus, pairs), ceil_div(pages, 8));
-  const int64_t even = pairs >= 8 * int64_t(num_cus)
-                           ? 1
-                           : std::min(pages / 96, 20 * int64_t(num_cus) / pairs);
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::max(fill, even), 1024)));
+  int32_t fill, even;
+  ranges_of_device(int64_t(prob->batch) * prob->num_kv_heads, num_cus, &fill, &even);
+  const int ranges = decode_ranges(static_cast<int>(most_pages(prob, view)), fill, even);
+  return std::min(ranges, 1024);
 }
 
 extern "C" pkv_status pkv_attend_window(const pkv_problem* prob, const pkv_view* view,
@@ -369,8 +358,7 @@ extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* vi
   const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
   if (tiles < 0 || check_view(view) != PKV_OK || num_cus < 1 || num_cus > 1024) return 0;
   if (tiles == 0) return 1;
-  // Two workgroups a compute unit, as long as a split keeps eight steps of four
-  // pages.  Tiles: half of a row's last one on the average; the launch counts the
+  // Two workgroups a compute unit, as long as a split keeps its steps.  Tiles: half of a row's last one on the average; the launch counts the
   // real ones and cuts into fewer ranges where there are more.
   const int64_t rows = int64_t(num_tokens) * (prob->num_q_heads / prob->num_kv_heads);
   const int64_t likely = one_per_row ? tiles
@@ -379,5 +367,6 @@ extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* vi
   const int64_t fill = 2 * int64_t(num_cus) / (likely * prob->num_kv_heads);
   const int64_t keys = std::min<int64_t>(most_pages(prob, view) + ceil_div(num_tokens, 16),
                                          prob->max_pages_per_row);
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(fill, keys / 32)));
+  return static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>(fill, prompt_ranges(static_cast<int>(keys / 4)))));
 }

@@ -40,13 +40,44 @@ PKV_HD bool sees(int p, int t, int window, int sinks) {
   return t <= p && (window == 0 || t > p - window || t < sinks);
 }
 
+// Ranges that the longest row of a decode call, `pages` visible pages, is worth
+// cutting into: `fill` of them fill the compute units once, `even` take them
+// several times.
+//  * Up to 40 pages stay whole: joining waits for stores, a counter and loads, 3
+//    us.  One row, 8 heads, in one range and in as many as fill: 24 pages 6.0 and
+//    7.5 us, 40 pages 7.8 and 7.7 (16 bits: 6.3 and 7.4, 8.4 and 7.6), 64 pages 10.3
+//    and 7.9.
+//  * One range for every compute unit, as long as a range keeps eight pages (one
+//    unit for each wave); beyond that ranges of at least 96 pages, so that rows of
+//    different lengths even out (the launch takes fewer where that comes out even).
+//    Joining costs more than it gives where ranges are shorter: 512 pairs of 64 to
+//    2048 pages took 237 us in up to 4, 222 in 6, 212 in 10 and 231 in 24 ranges each.
+// The host asks for the pages of a table, the launch again for those that there are:
+// under a table of 131072 tokens, with the table's ranges and with the rows' own,
+// 8 rows of 2048 tokens (4 bits, 8 heads) took 40 and 12 us, 64 rows of 1024 52 and 21.
+PKV_HD int decode_ranges(int pages, int fill, int even) {
+  const int own = pages <= 40 ? 1 : (fill < (pages + 7) / 8 ? fill : (pages + 7) / 8);
+  const int more = even < pages / 96 ? even : pages / 96;
+  return own > more ? own : (more > 1 ? more : 1);
+}
+
+// The same of a prompt's longest tile, `steps` of four visible pages: a range keeps
+// kRangeSteps (16 new tokens behind 2048, 64 heads over 8, the same table: 54 us with
+// the table's ranges, 23 with the rows').
+constexpr int kRangeSteps = 8;
+PKV_HD int prompt_ranges(int steps) {
+  return steps >= 2 * kRangeSteps ? steps / kRangeSteps : 1;
+}
+
 struct AttendArgs {
   const void* q;        // [B][Hq][d]
   const void* k_pool;   // 16-bit pages, or the 4-bit pool (v_pool unused)
   const void* v_pool;
   const int32_t* block_table;
   const int32_t* seq_lens;
-  int32_t cus;          // compute units of the device, set by the launcher
+  int32_t cus;          // compute units of the device; set by the launcher, as the
+  int32_t fill;         // next two, for decode_ranges
+  int32_t even;
   float* st_ml;         // [slots][G][2]: running max (log2 units) and sum
   float* st_o;          // [slots][G][d]
   int32_t* arrivals;    // [B * Hkv], zero between calls
@@ -85,6 +116,7 @@ struct PromptArgs {
   int32_t max_pages;
   int32_t num_pool_pages;
   int32_t splits;
+  int32_t tile_pages;   // that one tile sees at most
   int32_t window;
   int32_t sinks;
   float scale_log2;     // |scale| log2(e), above zero (subnormal where need be)
@@ -143,6 +175,15 @@ PKV_HD int64_t tile_base(int64_t off, int64_t row, int group) {
 inline size_t prompt_state_floats(int head_dim) { return 256 * (size_t(head_dim) / 2 + 2); }
 inline int64_t prompt_tiles(const PromptArgs& a) {
   return a.tok_offsets ? tile_base(a.num_tokens, a.batch, a.group) : int64_t(a.batch);
+}
+
+// `fill` and `even` of decode_ranges, for pairs of row and KV head.  Up to twenty
+// ranges a compute unit; eight pairs a unit come out even whole: 1024 pairs of up to
+// 1024 pages 235 us whole and 219 in 3 to 5 ranges, 2048 of up to 512 222 and 222, 4096
+// of up to 256 213 and 253 in 2.
+inline void ranges_of_device(int64_t pairs, int cus, int32_t* fill, int32_t* even) {
+  *fill = static_cast<int32_t>((cus + pairs - 1) / pairs);
+  *even = pairs >= 8 * int64_t(cus) ? 1 : static_cast<int32_t>(20 * int64_t(cus) / pairs);
 }
 
 // Compute units of the current device; 0 where the query fails.

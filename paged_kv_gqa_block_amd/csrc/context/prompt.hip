@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   const int window = a.window > 0 ? a.window : 0x7fffffff;
   const SeenPages sp = seen_pages(p_first, p_last, a.window, a.sinks);
   const int all_steps = (sp.count + 3) >> 2;
-  const int per_split = (all_steps + splits - 1) / splits;
+  const int per_split = max(found.steps, (all_steps + splits - 1) / splits);
   const int s_begin = split * per_split, s_end = min(s_begin + per_split, all_steps);
   if (s_begin >= s_end) return;
   const int32_t* bt = a.block_table + int64_t(run.row) * a.max_pages;

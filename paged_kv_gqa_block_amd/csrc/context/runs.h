@@ -67,18 +67,21 @@ __device__ __forceinline__ Run single_run(const Args& a, int row) {
 struct TileRun {
   Run run;
   int tile;    // of the run; negative: none
-  int splits;  // ranges that every tile's keys are cut into
+  int splits;  // ranges that a tile's keys are cut into, at most,
+  int steps;   // each of this many steps at least
 };
 
 // The share of workgroup `ts` of one KV head.  With max_splits > 1 the tiles are
 // counted first, so that tiles times ranges fill `slots` workgroups a KV head
-// and no more.
+// and no more, and no more ranges than the longest row's steps are worth; a shorter
+// tile's ranges are as long as the longest one's.
 template <typename Args>
 __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, int slots) {
   const int lane = threadIdx.x & 63;
   TileRun t;
   t.tile = -1;
   t.splits = a.splits;
+  t.steps = a.splits > 1 ? kRangeSteps : 0;
   if (!a.tok_offsets) {
     if (a.splits > 1) t.splits = min(a.splits, max(slots / a.batch, 1));
     const int row = ts / t.splits;
@@ -102,14 +105,19 @@ __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, i
   load(0);
   if (a.splits > 1) {
     int total = __builtin_amdgcn_readlane(count, 63);
+    int longest = next > first ? clean_len(len, a.max_pages) : 0;  // of rows with new tokens
     if (a.batch > 64) {
       for (int r0 = 64; r0 < a.batch; r0 += 64) {
         load(r0);
         total += __builtin_amdgcn_readlane(count, 63);
+        if (next > first) longest = max(longest, clean_len(len, a.max_pages));
       }
       load(0);
     }
-    t.splits = min(a.splits, max(slots / max(total, 1), 1));
+    longest = wave_max(longest);
+    const int steps = min((longest >> 6) + ((longest & 63) ? 1 : 0), (a.tile_pages + 3) >> 2);
+    t.splits = min(min(a.splits, prompt_ranges(steps)), max(slots / max(total, 1), 1));
+    t.steps = (steps + t.splits - 1) / t.splits;
   }
   const int item = ts / t.splits;
   if (item >= tiles) return t;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import context as oc
-from paged_kv_gqa_block_amd import engine
+from paged_kv_gqa_block_amd import _context, engine
 from tests.context_cases import TORCH, Batch, check, f64, lse_bound, out_bound
 from tests.parity import say
 
@@ -314,3 +314,232 @@ def test_smallest_scales_of_the_largest_products(scale, kv4, many):
     out, lse = step.run(b.device())
     torch.cuda.synchronize()
     _within(out, lse, b.reference(), "bf16", 128, b.vmax, many, f"scale {scale}")
+
+
+# ---- ranges ----------------------------------------------------------------------------------
+# What the header says of them, in plain numbers: the caps, and which states a launch writes.
+
+def _cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _decode_ranges(pages, pairs):
+    fill = -(-_cus() // pairs)
+    even = 1 if pairs >= 8 * _cus() else 20 * _cus() // pairs
+    own = 1 if pages <= 40 else min(fill, -(-pages // 8))
+    return max(own, min(even, pages // 96), 1)
+
+
+def _decode_plan(pages, hkv, cap):
+    """(ranges of every row, rounds of workgroups before evening out, whether the
+    ranges were made longer to come out even)."""
+    pages = np.asarray(pages)
+    t_max, rows = int(pages.max()), len(pages)
+
+    def ranges(per):
+        return np.maximum(1, -(-pages // per))
+    per = first = max(1, -(-t_max // min(cap, _decode_ranges(t_max, rows * hkv))))
+    total = int(ranges(per).sum())
+    rounds = -(-total * hkv // _cus())
+    if 1 < rows <= 64 and 2 <= rounds <= 4 and cap > 1:
+        even, t = (rounds - 1) * _cus() // hkv, total
+        for _ in range(3):
+            if t <= even or even < rows:
+                break
+            per = min(per + 1 + int(np.float32(per) * np.float32(t - even) / np.float32(even)), t_max)
+            t = int(ranges(per).sum())
+        if t > even or (rounds - 1) * (per + 8) >= rounds * (first + 8):
+            per = first
+    return ranges(per), rounds, per != first
+
+
+def _decode_states(step, rows, hkv, group):
+    """Ranges of every (row, KV head) whose state the last call wrote."""
+    n = rows * hkv * step.splits * group * 2 * 4
+    ml = step.workspace[256 << 10:(256 << 10) + n].view(torch.float32)
+    return (~torch.isnan(ml.view(rows, hkv, step.splits, group * 2))).all(-1).sum(-1).cpu().numpy()
+
+
+def _checked_decode(b, cap, wide=None):
+    """Run, compare with the oracle and the expected ranges; (step, rounds, evened)."""
+    w, prob = b.device(), b.problem()
+    if wide:
+        table = torch.zeros(len(b.lens), wide, dtype=torch.int32, device="cuda")
+        table[:, :w["block_table"].shape[1]] = w["block_table"]
+        w["block_table"], prob = table, b.problem(max_pages_per_row=wide)
+    step = (engine.Kv4Step if b.kv4 else engine.WindowStep)(prob, b.window, b.sinks, cap)
+    step.workspace[256 << 10:] = 255  # NaN, in every state
+    out, lse = step.run(w)
+    torch.cuda.synchronize()
+    pages = [-(-int(n) // 16) for n in b.lens]
+    want, rounds, evened = _decode_plan(pages, b.hkv, step.splits)
+    got = _decode_states(step, len(b.lens), b.hkv, b.group)
+    assert (got == np.where(want > 1, want, 0)[:, None]).all(), (got.tolist(), want.tolist())
+    check(out, lse, b.reference(), b.dtype, b.d, b.vmax, False, "ranges")
+    assert not step.workspace[:256 << 10].any()
+    return step, rounds, evened
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("rows,length,hkv", [(1, 100, 2), (1, 640, 2), (1, 641, 2), (2, 1100, 1),
+                                             (8, 384, 2), (8, 1300, 2), (3, 3300, 1)])
+def test_short_rows_under_a_wide_table(rows, length, hkv, kv4):
+    """Ranges follow the rows that there are: the bits of a table as wide as the
+    rows, and rows of up to 40 pages whole."""
+    say(f"[wide table] rows={rows} length={length} Hkv={hkv} kv4={kv4}")
+    lens = [length - 5 * i for i in range(rows)]
+    b = Batch(61, lens, hkv=hkv, group=4, kv4=kv4)
+    tight, _, _ = _checked_decode(b, None)
+    for wide in (2048, 8192):
+        step, _, _ = _checked_decode(b, None, wide)
+        assert step.splits > tight.splits
+        assert _same(step.out, tight.out) and _same(step.lse, tight.lse)
+
+
+EVENED = [(5, 900, 1000, 8, True), (9, 700, 720, 8, True), (20, 660, 700, 8, True),
+          (40, 100, 700, 8, False), (60, 700, 900, 1, True), (30, 650, 1000, 2, True),
+          (64, 641, 650, 3, True), (60, 3050, 3060, 5, False)]
+
+
+@pytest.mark.parametrize("rows,low,high,hkv,evened,kv4",
+                         [(*e, kv4) for e in EVENED for kv4 in (False, True)
+                          if not kv4 or e[2] < 3000])
+def test_ranges_evened_out(rows, low, high, hkv, evened, kv4):
+    """Two to four rounds of workgroups: longer ranges where those come out even and
+    cost less, the first ones otherwise."""
+    lens = np.random.default_rng(rows).integers(low, high + 1, rows)
+    lens[0] = high
+    b = Batch(62, lens, hkv=hkv, group=1, d=64, kv4=kv4, dtype="bf16")
+    say(f"[evened] rows={rows} {low}..{high} Hkv={hkv} kv4={kv4}")
+    _, rounds, got = _checked_decode(b, 64)
+    if _cus() == 256:  # the sizes above are chosen for a whole card
+        assert 2 <= rounds <= 4 and got == evened, (rounds, got)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 9, 16])
+def test_joins_of_every_group(group, kv4):
+    """Sixteen ranges and more of one row, joined by every number of heads."""
+    for d in (64, 128):
+        say(f"[joins] G={group} d={d} kv4={kv4}")
+        b = Batch(63, [2100], hkv=1, group=group, d=d, kv4=kv4)
+        for cap in (None, 2, 5, 300):
+            _checked_decode(b, cap, 200)
+
+
+def _prompt_states(step, tiles, hkv, d):
+    slot = 256 * (d // 2 + 2)
+    st = step.workspace[256 << 10:].view(torch.float32)
+    st = st[:tiles * hkv * step.splits * slot].view(tiles, hkv, step.splits, slot)
+    return (~torch.isnan(st[..., -512:])).all(-1).sum(-1).cpu().numpy()
+
+
+def _prompt_plan(b, cap, hkv):
+    """Ranges of every tile, rows' last tiles first."""
+    per_row = [-(-int(m) * b.group // 128) for m in b.new]
+    longest = max([-(-int(n) // 64) for n, m in zip(b.lens, b.new) if m], default=0)
+    slots = 2 * _cus() // hkv
+    splits = min(cap, longest // 8 if longest >= 16 else 1, max(slots // max(sum(per_row), 1), 1))
+    least = -(-longest // splits)
+    out = []
+    for n, m, tiles in zip(b.lens, b.new, per_row):
+        for tile in reversed(range(tiles)):
+            last = int(n) - int(m) + min((tile + 1) * 128 - 1, int(m) * b.group - 1) // b.group
+            steps = -(-(last // 16 + 1) // 4)
+            ns = -(-steps // max(least, -(-steps // splits)))
+            out.append(ns if ns > 1 else 0)
+    return out
+
+
+@pytest.mark.parametrize("kv4,d,dtype", [(False, 128, "bf16"), (False, 64, "f16"), (True, 128, "f16")])
+@pytest.mark.parametrize("lens,new", [
+    ([5000], [1]), ([4000, 700, 100], [33, 5, 100]), ([1024], [1024]), ([200, 90], [20, 90]),
+    ([1023, 2500, 0], [60, 70, 0])])
+def test_prompt_ranges_follow_the_rows(lens, new, kv4, d, dtype):
+    """Ranges of a prompt: eight steps or more each, in a table as wide as the rows
+    and in a wide one, with the same bits."""
+    b = Batch(64, lens, new, hkv=2, group=2, d=d, dtype=dtype, kv4=kv4)
+    w, n = b.device(), int(b.new.sum())
+    ref, outs = b.reference(), []
+    for wide, cap in ((None, None), (8192, None), (8192, 3), (8192, 200)):
+        say(f"[prompt ranges] {lens} {new} kv4={kv4} d={d} {dtype} wide={wide} cap={cap}")
+        x, prob = w, b.problem()
+        if wide:
+            table = torch.zeros(len(lens), wide, dtype=torch.int32, device="cuda")
+            table[:, :w["block_table"].shape[1]] = w["block_table"]
+            x, prob = dict(w, block_table=table), b.problem(max_pages_per_row=wide)
+        step = engine.PromptStep(prob, n, splits=cap)
+        step.workspace[256 << 10:] = 255
+        out, lse = step.run(x)
+        torch.cuda.synchronize()
+        check(out, lse, ref, dtype, d, b.vmax, True, f"wide {wide} cap {cap}")
+        plan = _prompt_plan(b, step.splits, 2)
+        if step.splits > 1:
+            got = _prompt_states(step, len(plan), 2, d)
+            assert (got == np.array(plan)[:, None]).all(), (got.tolist(), plan)
+            assert not step.workspace[:256 << 10].any()
+        outs.append((plan, out.clone(), lse.clone()))
+    for plan, out, lse in outs[1:]:
+        if plan == outs[0][0]:
+            assert _same(out, outs[0][1]) and _same(lse, outs[0][2])
+
+
+def test_prompt_ranges_behind_a_window():
+    """A window over long rows: ranges of the pages that a tile sees, not of the row."""
+    b = Batch(65, [6000, 3000], [40, 3], hkv=1, group=4, window=1500, sinks=20)
+    w = b.device()
+    for cap in (None, 2, 50):
+        say(f"[prompt window ranges] cap={cap}")
+        step = engine.PromptStep(b.problem(), 43, 1500, 20, cap)
+        step.workspace[256 << 10:] = 255
+        out, lse = step.run(w)
+        torch.cuda.synchronize()
+        check(out, lse, b.reference(), "f16", 128, b.vmax, True, f"cap {cap}")
+        used = _prompt_states(step, 3, 1, 128)
+        assert (used == (2 if cap == 2 else 3)).all(), used.tolist()
+
+
+@pytest.mark.parametrize("rows", [64, 70])
+def test_prompt_ranges_of_many_rows(rows):
+    """Rows around and beyond what a wave holds, in ranges, one of them long."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, 900, rows)
+    lens[rows - 3] = 3500
+    new = np.minimum(lens, rng.integers(0, 9, rows) * (rng.random(rows) < 0.5))
+    new[rows - 3] = 20
+    say(f"[prompt ranges of many rows] {rows}")
+    b = Batch(66, lens, new, hkv=1, group=2, d=64, dtype="bf16")
+    step = engine.PromptStep(b.problem(), int(new.sum()), splits=6)
+    step.workspace[256 << 10:] = 255
+    out, lse = step.run(b.device())
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "bf16", 64, b.vmax, True, f"{rows} rows")
+    plan = _prompt_plan(b, 6, 1)
+    got = _prompt_states(step, len(plan), 1, 64)
+    assert max(plan) > 1 and (got == np.array(plan)[:, None]).all(), (got.tolist(), plan)
+
+
+def test_one_workspace_for_ranges_of_all_kinds():
+    """Calls whose pairs and tiles are really cut share one workspace in turn."""
+    steps = []
+    for i, (lens, new, hkv, cap) in enumerate((
+            ([900, 33], None, 2, 40), ([700] * 30, None, 2, 3), ([2000], None, 1, 100),
+            ([1500, 2400], [90, 40], 3, 4), ([1100], [1], 8, 30))):
+        b = Batch(70 + i, lens, new, hkv=hkv, group=2, d=64)
+        step = (engine.PromptStep(b.problem(), int(b.new.sum()), splits=cap) if new
+                else _step(b, cap))
+        steps.append((b, step, b.device(), new is not None, b.reference()))
+    shared = torch.zeros(max(x[1].workspace.numel() for x in steps), dtype=torch.uint8, device="cuda")
+    for b, step, w, many, ref in steps + steps[::-1]:
+        say(f"[shared ranges] B={len(b.lens)} Hkv={b.hkv} cap={step.splits} prompt={many}")
+        head = (b.problem(), step.view)
+        if many:
+            _context.pkv_prompt_window(*head, w["tok_offsets"], step.num_tokens, w["seq_lens"],
+                                       step.splits, w["q"], w["k_pool"], w["v_pool"],
+                                       w["block_table"], shared, step.out, step.lse)
+        else:
+            _context.pkv_attend_window(*head, w["seq_lens"], step.splits, w["q"], w["k_pool"],
+                                       w["v_pool"], w["block_table"], shared, step.out, step.lse)
+        torch.cuda.synchronize()
+        check(step.out, step.lse, ref, "f16", 64, b.vmax, many, "shared ranges")
+        assert not shared[:256 << 10].any()
