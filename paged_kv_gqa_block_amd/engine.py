@@ -200,13 +200,16 @@ class _ContextCalls:
     stream.  Its memory is not reused before work on a torch stream that it was
     given is done; a stream given as a number is not torch's to wait for, so
     keep the object until that work is done.  The caller's buffers have to be
-    ready on the stream of a call, and live until its work is done (until the
-    last call of a bound form), as with every torch call."""
+    ready on the stream of a call and live until its work is done, as with every
+    torch call.  A bound form and a captured graph hold addresses alone: keep the
+    object and the buffers as long as those are used."""
 
     def __init__(self, prob: _lib.pkv_problem, device):
         self.prob = prob
         self.device = torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
+        if self.device.type != "cuda":
+            raise ValueError(f"the context operators run on a GPU, not on {self.device}")
+        if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
         self.dtype = torch.bfloat16 if prob.dtype == _lib.PKV_BF16 else torch.float16
