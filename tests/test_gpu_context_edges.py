@@ -543,3 +543,45 @@ def test_one_workspace_for_ranges_of_all_kinds():
         torch.cuda.synchronize()
         check(step.out, step.lse, ref, "f16", 64, b.vmax, many, "shared ranges")
         assert not shared[:256 << 10].any()
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_binding_and_engine_make_the_same_calls(kv4):
+    """The plain binding of every entry point against the classes: the same bits."""
+    b = Batch(80, [900, 0, 333], [40, 0, 333], hkv=2, group=4, kv4=kv4, window=500, sinks=4)
+    w, prob = b.device(), b.problem()
+    n = int(b.new.sum())
+    x = torch.randn(n, 2, 2, 128, generator=torch.Generator().manual_seed(2)).half().cuda()
+    k, v = x[:, 0], x[:, 1]
+    run = (w["tok_offsets"], n, w["seq_lens"])
+    say(f"[binding] kv4={kv4}")
+    if kv4:
+        mine, cache = w["kv4_pool"].clone(), engine.Kv4Cache(prob, pool=w["kv4_pool"])
+        cache.store(k, v, w["block_table"], w["seq_lens"], w["tok_offsets"])
+        _context.pkv_kv4_store(prob, *run, k, v, w["block_table"], mine)
+        outs = [[torch.empty(n, 2, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+                for _ in range(2)]
+        cache.load(w["block_table"], w["seq_lens"], w["tok_offsets"], *outs[0])
+        _context.pkv_kv4_load(prob, *run, w["block_table"], mine, *outs[1])
+        torch.cuda.synchronize()
+        assert _same(mine, w["kv4_pool"]) and all(_same(a, c) for a, c in zip(*outs))
+        pools = (mine,)
+    else:
+        mine = w["k_pool"].clone(), w["v_pool"].clone()
+        engine.store_kv(prob, k, v, w["block_table"], w["seq_lens"], w["tok_offsets"],
+                        w["k_pool"], w["v_pool"])
+        _context.pkv_store_kv(prob, *run, k, v, w["block_table"], *mine)
+        torch.cuda.synchronize()
+        assert _same(mine[0], w["k_pool"]) and _same(mine[1], w["v_pool"])
+        pools = mine
+    for step, q in ((_step(b), w["q"][:3].contiguous()),
+                    (engine.PromptStep(prob, n, 500, 4, 3), w["q"])):
+        out, lse = (t.clone() for t in step.run(dict(w, q=q)))
+        got, got_lse = torch.zeros_like(out), torch.zeros_like(lse)
+        many = isinstance(step, engine.PromptStep)
+        fn = {(False, False): _context.pkv_attend_window, (False, True): _context.pkv_attend_kv4,
+              (True, False): _context.pkv_prompt_window, (True, True): _context.pkv_prompt_kv4}
+        head = (prob, step.view, *(run if many else (w["seq_lens"],)), step.splits, q)
+        fn[many, kv4](*head, *pools, w["block_table"], step.workspace, got, got_lse)
+        torch.cuda.synchronize()
+        assert _same(out, got) and _same(lse, got_lse)
