@@ -196,10 +196,12 @@ class _ContextCalls:
     (include/pkv_context.h).  They run on the device of their buffers, on the
     given stream or that device's current one.
 
-    What an object allocates is ready when its constructor returns, for every
-    stream.  Its memory is not reused before work on a torch stream that it was
-    given is done; a stream given as a number is not torch's to wait for, so
-    keep the object until that work is done.  The caller's buffers have to be
+    The first call on a stream waits for the fills of what the object allocated,
+    and its memory is not reused before work on the torch streams that it was
+    given is done.  A stream given as a number is not torch's to watch: keep the
+    object until work on it is done.  A stream that is being captured cannot
+    wait: build the object inside the capture, or let the device finish first
+    (torch.cuda.graph does).  The caller's buffers have to be
     ready on the stream of a call and live until its work is done, as with every
     torch call.  A bound form and a captured graph hold addresses alone: keep the
     object and the buffers as long as those are used."""
@@ -223,24 +225,44 @@ class _ContextCalls:
                         "token": (p.num_kv_heads, p.head_dim),
                         "q": (p.batch, p.num_q_heads, p.head_dim)}
         self._prob_ref = ctypes.byref(prob)
-        self._buffers, self._streams = (), set()
+        self._buffers, self._ready = (), None
+        self._waited, self._known = set(), set()  # streams: ordered, and recorded too
 
     def _own_buffers(self, *buffers: torch.Tensor) -> None:
-        """Take charge of buffers just allocated on the current stream."""
-        _await_buffers(self.device)
+        """Take charge of buffers just allocated and filled on the current stream."""
         self._buffers = buffers
-        self._streams = {torch._C._cuda_getCurrentRawStream(self._index)}
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                self._ready = torch.cuda.Event()
+                self._ready.record()
+            home = torch.cuda.current_stream().cuda_stream
+        self._waited, self._known = {home}, {home}
+
+    def _meet(self, handle: int, stream) -> None:
+        """Order a stream behind the fills of the object's buffers, and have their
+        memory wait for it."""
+        number = isinstance(stream, int)
+        if handle not in self._waited and self._ready is not None:  # None: built in a capture
+            with torch.cuda.device(self.device):
+                if torch.cuda.is_current_stream_capturing():
+                    return
+                at = (torch.cuda.ExternalStream(handle) if number
+                      else torch.cuda.current_stream() if stream is None else stream)
+                at.wait_event(self._ready)
+        self._waited.add(handle)
+        if not number:  # of a number nobody knows how long its stream lives
+            at = torch.cuda.current_stream(self.device) if stream is None else stream
+            for t in self._buffers:
+                t.record_stream(at)
+            self._known.add(handle)
 
     def _stream(self, stream) -> int:
         if stream is None:
             handle = torch._C._cuda_getCurrentRawStream(self._index)
         else:
             handle = stream if isinstance(stream, int) else stream.cuda_stream
-        if handle not in self._streams and not isinstance(stream, int):
-            at = torch.cuda.current_stream(self.device) if stream is None else stream
-            for t in self._buffers:
-                t.record_stream(at)
-            self._streams.add(handle)
+        if self._buffers and handle not in self._known:
+            self._meet(handle, stream)
         return handle
 
     def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> int:

@@ -94,20 +94,27 @@ def _of_kind(kind):
     return b, b.device(), make
 
 
+@pytest.mark.parametrize("given", ["argument", "number", "current", "bound"])
 @pytest.mark.parametrize("kind", KINDS)
-def test_step_built_on_a_busy_stream_runs_on_another(kind):
-    """The workspace's counters are zero and its memory free when the constructor
-    returns, whatever still runs on the stream that it was built on."""
+def test_step_built_on_a_busy_stream_runs_on_another(kind, given):
+    """The workspace's counters are zero and its memory free before the first call
+    on any stream, whatever still runs on the stream that it was built on."""
     b, w, make = _of_kind(kind)
     sizes = [t.numel() * t.element_size() for t in (lambda s: (s.workspace, s.out, s.lse))(make())]
     building, running = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
-    say(f"[built elsewhere] {kind}")
+    say(f"[built elsewhere] {kind} {given}")
     with torch.cuda.stream(building):
         _litter(sizes)
         _busy(building)
         step = make()
-    out, lse = step.run(w, running)
+    if given == "current":
+        with torch.cuda.stream(running):
+            out, lse = step.run(w)
+    elif given == "bound":
+        out, lse = step.run_bound(step.bind(w, running))
+    else:
+        out, lse = step.run(w, running if given == "argument" else running.cuda_stream)
     running.synchronize()
     check(out, lse, b.reference(), "f16", 128, b.vmax, kind == "prompt", kind)
     torch.cuda.synchronize()
