@@ -30,7 +30,8 @@
 // tokens (1.21 GB): 212-227 us, 5.3-5.7 TB/s; the same pages read and not used take
 // 187 us (6.5 TB/s), the rest is conversion and matrix work that three waves do
 // not hide (221 vector instructions for two pages).  Eight rows, half of them
-// short (111 MB): 28-29 us.  One row of 32768: 15-16 us.  16 bits, window 1000 and
+// short (111 MB): 28-29 us.  One row of 32768: 15-16 us.  256 rows of 1024-2048 over
+// one KV head 18 us (3.0 TB/s), 1024 rows of 256-512 over eight 109 (4.2).  16 bits, window 1000 and
 // 5 sinks (260 MB): 44 us, 5.9 TB/s; window 4096 over eight rows (134 MB): 27 us,
 // 5.0 TB/s.  Small calls: 7 us, a chain of dependent loads (length, page number,
 // page, state, counter).

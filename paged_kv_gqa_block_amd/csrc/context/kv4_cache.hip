@@ -6,8 +6,9 @@
 // are e2m1 roundings of x / 2^e, ties to even, saturating.  Bound: bytes moved;
 // there is no reuse and no arithmetic to speak of.  Measured: 98000 tokens of 8
 // KV heads, d = 128, f16: 117 us to quantise 401 MB into 107 MB (4.3 TB/s),
-// 107 us to read them back (4.7 TB/s; a plain copy of this size reaches 4.9);
-// one token of 64 rows: 3.4 and 3.1 us, a launch and its loads.
+// 107 us to read them back (4.7 TB/s; a plain copy of this size reaches 4.9), 155
+// to write them in 16 bits (5.2 TB/s); one token of 64 rows: 3.4, 3.1 and 3.1 us, a
+// launch and its loads.
 //
 // One workgroup per (page of a row that the run touches, KV head): 16 tokens
 // by d channels.  Thread (token, chunk) converts eight channels of K and of V;

@@ -9,8 +9,8 @@
 // 128 packed query rows (token-major, the G heads of a KV head side by side, so
 // that they share its keys) and walks the pages that any of them sees, 64 keys
 // a step through two LDS buffers; each of its four waves owns 32 rows.  Few
-// tiles over many keys are cut along the keys (splits), and the last split of
-// a tile to finish joins the partial states.
+// tiles over many keys are cut along the keys (splits, of eight steps and more), and
+// the last split of a tile to finish joins the partial states.
 //  * S^T = K Q^T on v_mfma_f32_32x32x16: a lane holds one query's scores for 16
 //    of 32 keys, so maximum and sum need one exchange with the lane 32 away.
 //  * O^T += V^T P^T: the lane's own probabilities are the B operand as they
@@ -27,16 +27,17 @@
 // own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
 // last rounding.
 //
-// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 396-412 us
-// for 413 GFLOP, 1.00-1.04 PFLOP/s, 0.83-0.86 of what a square product of 8192
-// reaches on the same card (over 4 bits: 385 us).  Matrix work fills half of a SIMD's cycles
-// and vector work (exponentials, maxima, rounding) 45 %, and the two hardly
-// overlap.  Direct loads and two scores in flight brought it from 502 us; deeper
-// rings of buffers, pages touched ahead in L2 (430 us), wave priorities and tiles
-// of 64 rows brought nothing.  Eight chunks of 9-54 tokens behind a window of
-// 4096, 64 heads over 8: 61-66 us, of which 46 at the same rate, 8 until the first
-// pages are there (dependent loads) and 8 for the last join (65 KiB of state a
-// tile and range).  Eight prompts of 183-1659 tokens, d = 64, window 500: 20 us.
+// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 402-420 us
+// for 413 GFLOP, card by card, 0.98-1.03 PFLOP/s, 0.82-0.85 of what a square product
+// of 8192 reaches (over 4 bits: 409 us beside 408).  Matrix work fills half of a
+// SIMD's cycles and vector work (exponentials, maxima, rounding) 47 %, and the two
+// hardly overlap.  Direct loads and two scores in flight brought it from 502 us;
+// deeper rings of buffers, pages touched ahead in L2 (430 us), wave priorities and
+// tiles of 64 rows brought nothing.  Eight chunks of 9-54 tokens behind a window of
+// 4096, 64 heads over 8: 65-69 us (4 bits: 67), of which 46 at the same rate, 8 until
+// the first pages are there (dependent loads) and 8 for the last join (65 KiB of
+// state a tile and range).  Eight prompts of 183-1659 tokens, d = 64, window 500:
+// 20 us (4 bits: 24).
 #include "context_internal.h"
 #include "kv4_common.h"
 #include "mfma.h"

@@ -32,7 +32,8 @@ __device__ __forceinline__ float4 get_state4(const float* head, int c) {
 }
 
 // Arrival counter of pair k < 65536: the first 2048 lie on cache lines of their
-// own, so that atomics of different pairs never share one.  (With 8 pairs of 32
+// own, so that atomics of different pairs never share one (256 compute units are
+// worth ranges for no more pairs than that).  (With 8 pairs of 32
 // arrivals it makes no difference: the last arrival takes 2.1-2.4 us either way.)
 __device__ __forceinline__ int32_t* arrival_counter(int32_t* arrivals, int64_t k) {
   return arrivals + ((k & 2047) << 5) + (k >> 11);
