@@ -69,9 +69,12 @@ PKV_HD int prompt_ranges(int steps) {
   return steps >= 2 * kRangeSteps ? steps / kRangeSteps : 1;
 }
 
+// How a cache holds K and V.
+enum class Cache { k16, k4, k8 };
+
 struct AttendArgs {
   const void* q;        // [B][Hq][d]
-  const void* k_pool;   // 16-bit pages, or the 4-bit pool (v_pool unused)
+  const void* k_pool;   // 16-bit pages, or the 4-bit or 8-bit pool (v_pool unused)
   const void* v_pool;
   const int32_t* block_table;
   const int32_t* seq_lens;
@@ -94,6 +97,12 @@ struct AttendArgs {
   int32_t sinks;
   float scale_log2;     // |scale| log2(e), above zero (subnormal where need be)
   uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
+  const uint8_t* scales;       // 8 bits: [pages][Hkv][2]
+  // Cross attention alone: q, out [num_tokens][Hq][d], a slot's states are those of
+  // kCrossRows queries.
+  const int32_t* tok_offsets;  // [B + 1]; null: one token per row
+  int32_t num_tokens;
+  uint32_t group_inv;   // ceil(4096 / group)
 };
 
 struct PromptArgs {
@@ -103,7 +112,7 @@ struct PromptArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* tok_offsets;  // [B + 1]
-  float* state;         // splits' states, see prompt.hip
+  float* state;         // splits' states, see prompt_kernel.h
   int32_t* arrivals;    // [tiles * Hkv], zero between calls
   void* out;
   float* lse;
@@ -121,6 +130,7 @@ struct PromptArgs {
   int32_t sinks;
   float scale_log2;     // |scale| log2(e), above zero (subnormal where need be)
   uint32_t q_flip;      // sign bits of a negative scale, moved to the queries
+  const uint8_t* scales;  // 8 bits: [pages][Hkv][2]
 };
 
 struct StoreArgs {
@@ -171,7 +181,12 @@ constexpr int kTileRows = 128;
 PKV_HD int64_t tile_base(int64_t off, int64_t row, int group) {
   return off * group / kTileRows + row;
 }
-// Floats of one split's state of one tile and KV head (prompt.hip).
+// Tiles of few queries in cross attention, by the same rule.
+constexpr int kCrossRows = 16;
+PKV_HD int64_t cross_tile_base(int64_t off, int64_t row, int group) {
+  return off * group / kCrossRows + row;
+}
+// Floats of one split's state of one tile and KV head (prompt_kernel.h).
 inline size_t prompt_state_floats(int head_dim) { return 256 * (size_t(head_dim) / 2 + 2); }
 inline int64_t prompt_tiles(const PromptArgs& a) {
   return a.tok_offsets ? tile_base(a.num_tokens, a.batch, a.group) : int64_t(a.batch);

@@ -1,0 +1,288 @@
+// Page tables kept on the device (gfx950): pages for a step's new tokens, with the
+// offsets, lengths, slots and positions that the step's calls read, and pages given
+// back.
+//
+//   off_i = sum_{k<i} c_k,  need_i = ceil((n_i + c_i) / 16) - ceil(n_i / 16),
+// row i is served where its tokens fit the call's arrays and the table and the sum of
+// need_k, k <= i, fits the free list; its page of rank m among all that are asked for
+// is free[count - 1 - m].  Released pages go on top, the last row's last page first, so
+// that giving back what a call took restores the list.
+//
+// Bound: latency.  A step of 64 rows reads and writes a few KB behind a chain of three
+// dependent loads (lengths, free list, table); 256 rows of 130000 tokens write
+// 1.6 MB.  So: one launch; every workgroup scans all rows by itself (1024 at a time,
+// four a thread) and does 512 tokens or its share of the pages.  Nothing that
+// the others read is written before all are done: the last of several workgroups to
+// finish writes lengths and counts; one workgroup needs nobody.
+#include "context/states.h"
+#include "context/wave.h"
+#include "serving/serving_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerThread = 4;
+constexpr int kChunk = kThreads * kRowsPerThread;  // rows of one scan
+constexpr int kTokens = 512;                       // new tokens of a workgroup
+constexpr int kFewPages = 1024;                    // released by one workgroup alone
+
+__device__ __forceinline__ int pages_of(int tokens) {
+  return (tokens >> 4) + ((tokens & 15) ? 1 : 0);
+}
+
+// Inclusive sum over the wave, no higher than `most` (<= 2^30 + 1).
+__device__ __forceinline__ uint32_t capped_scan(uint32_t x, uint32_t most) {
+  auto add = [&](int y) { x = min(x + static_cast<uint32_t>(y), most); };
+  add(moved<kDppRowShr + 1>(static_cast<int>(x)));
+  add(moved<kDppRowShr + 2>(static_cast<int>(x)));
+  add(moved<kDppRowShr + 4>(static_cast<int>(x)));
+  add(moved<kDppRowShr + 8>(static_cast<int>(x)));
+  add(moved<kDppRowBcast15, 0xa>(static_cast<int>(x)));
+  add(moved<kDppRowBcast31, 0xc>(static_cast<int>(x)));
+  return x;
+}
+
+// Sums before a thread's own values `x` over the workgroup, from `carry` on, which
+// becomes the sum of all; none above `most`.
+__device__ __forceinline__ uint32_t scan_before(uint32_t x, uint32_t& carry, uint32_t most,
+                                                uint32_t (&s_wave)[4]) {
+  const int wave = threadIdx.x >> 6;
+  const uint32_t upto = capped_scan(x, most);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) s_wave[wave] = upto;
+  // The lane below, 0 in the first.
+  uint32_t before = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(
+      ((static_cast<int>(threadIdx.x & 63) - 1) & 63) << 2, static_cast<int>(upto)));
+  if ((threadIdx.x & 63) == 0) before = 0;
+  __syncthreads();
+  uint32_t all = carry;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w == wave) before = min(before + all, most);
+    all = min(all + s_wave[w], most);
+  }
+  carry = all;
+  return before;
+}
+
+// Index of the first entry of v[0, n) above x, v not decreasing, its last above x.
+__device__ __forceinline__ int first_above(const uint32_t* v, int n, uint32_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int free_count(const int32_t* state, int pool) {
+  return min(max(state[kStateFree], 0), pool);
+}
+
+__global__ __launch_bounds__(kThreads) void take_kernel(TakeArgs a) {
+  __shared__ uint32_t s_upto[kChunk];  // tokens up to and with a row
+  __shared__ uint32_t s_off[kChunk];   // tokens before it
+  __shared__ uint32_t s_rank[kChunk];  // pages asked for before it
+  __shared__ int s_len[kChunk];        // tokens it holds; negative: not served
+  __shared__ uint32_t s_wave[4];
+  __shared__ bool s_last;
+  const int cap = a.max_pages * 16;
+  const uint32_t most = static_cast<uint32_t>(a.num_tokens) + 1;
+  const uint32_t begin = blockIdx.x * uint32_t(kTokens), end = begin + kTokens;
+  const int free = free_count(a.state, a.num_pool_pages);
+  bool finish = gridDim.x == 1;  // this workgroup writes the rows' results
+
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t tokens = 0, asked = 0, granted = 0, denied = 0;
+    for (int r0 = 0; r0 < a.batch; r0 += kChunk) {
+      const uint32_t tokens0 = tokens;
+      int cnt[kRowsPerThread], len[kRowsPerThread];
+      uint32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        const int r = r0 + int(threadIdx.x) * kRowsPerThread + i;
+        cnt[i] = r < a.batch ? max(a.counts[r], 0) : 0;
+        len[i] = r < a.batch ? a.lens[r] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i)
+        mine = min(mine + min(static_cast<uint32_t>(cnt[i]), most), most);
+      uint32_t before = scan_before(mine, tokens, most, s_wave);
+      uint32_t off[kRowsPerThread], upto[kRowsPerThread];
+      int need[kRowsPerThread];
+      bool ok[kRowsPerThread];
+      uint32_t wants = 0;
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        off[i] = before;
+        upto[i] = before = min(before + min(static_cast<uint32_t>(cnt[i]), most), most);
+        ok[i] = len[i] >= 0 && len[i] <= cap && cnt[i] <= cap - len[i] && upto[i] < most;
+        need[i] = ok[i] ? pages_of(len[i] + cnt[i]) - pages_of(len[i]) : 0;
+        wants += static_cast<uint32_t>(need[i]);
+      }
+      uint32_t rank = scan_before(wants, asked, 0x7fffffffu, s_wave);
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        const int at = int(threadIdx.x) * kRowsPerThread + i, r = r0 + at;
+        ok[i] = ok[i] && (need[i] == 0 || rank + need[i] <= static_cast<uint32_t>(free));
+        s_upto[at] = upto[i];
+        s_off[at] = off[i];
+        s_rank[at] = rank;
+        s_len[at] = ok[i] ? len[i] : -1;
+        rank += static_cast<uint32_t>(need[i]);
+        if (ok[i]) granted += static_cast<uint32_t>(need[i]);
+        if (r < a.batch && !ok[i] && cnt[i] > 0) ++denied;
+        if (finish && r < a.batch) {
+          a.seq_lens[r] = ok[i] ? len[i] + cnt[i] : 0;
+          a.tok_offsets[r + 1] = static_cast<int>(min(upto[i], most - 1));
+          if (ok[i]) a.lens[r] = len[i] + cnt[i];
+        }
+      }
+      __syncthreads();
+      if (pass == 0) {
+        const int rows = min(a.batch - r0, kChunk);
+        const uint32_t stop = min(min(tokens, most - 1), end);
+        for (uint32_t t = begin + threadIdx.x; t < stop; t += kThreads) {
+          if (t < tokens0) continue;
+          const int at = first_above(s_upto, rows, t);
+          const int held = s_len[at];
+          int64_t slot = -1;
+          int p = -1;
+          if (held >= 0) {
+            const int64_t row = int64_t(r0 + at) * a.max_pages;
+            p = held + static_cast<int>(t - s_off[at]);
+            const int entry = p >> 4, had = pages_of(held);
+            int page;
+            if (entry >= had) {
+              page = a.free_pages[free - 1 - static_cast<int>(s_rank[at]) - (entry - had)];
+              if ((p & 15) == 0) a.block_table[row + entry] = page;
+            } else {
+              page = a.block_table[row + entry];
+            }
+            if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pool_pages))
+              slot = int64_t(page) * 16 + (p & 15);
+          }
+          if (a.slots) a.slots[t] = slot;
+          if (a.positions) a.positions[t] = p;
+        }
+        if (!finish && tokens >= end) break;  // the rows behind have none of its tokens
+      }
+    }
+    if (finish) {
+      const uint32_t all = static_cast<uint32_t>(wave_sum_i(static_cast<int>(granted)));
+      const uint32_t no = static_cast<uint32_t>(wave_sum_i(static_cast<int>(denied)));
+      __shared__ uint32_t s_all[4], s_no[4];
+      if ((threadIdx.x & 63) == 0) {
+        s_all[threadIdx.x >> 6] = all;
+        s_no[threadIdx.x >> 6] = no;
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        a.tok_offsets[0] = 0;
+        a.state[kStateFree] = free - static_cast<int>(s_all[0] + s_all[1] + s_all[2] + s_all[3]);
+        a.state[kStateDenied] = static_cast<int>(s_no[0] + s_no[1] + s_no[2] + s_no[3]);
+      }
+      return;
+    }
+    if (!last_to_arrive(a.state + kStateArrivals, gridDim.x, &s_last)) return;
+    finish = true;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void release_kernel(ReleaseArgs a) {
+  __shared__ uint32_t s_upto[kChunk];  // pages up to and with a row, from the last row on
+  __shared__ int s_end[kChunk];        // block-table entry behind its last page
+  __shared__ uint32_t s_wave[4];
+  __shared__ bool s_last;
+  const int cap = a.max_pages * 16;
+  const int free = free_count(a.state, a.num_pool_pages);
+  // The new length of a row: `keep` where that is shorter.
+  auto kept = [&](int r, int& len) {
+    len = a.lens[r];
+    const int keep = a.keep[r];
+    return (len < 0 || len > cap || keep < 0 || keep >= len) ? len : keep;
+  };
+  auto pages_between = [&](int keep, int len) {
+    return (len < 0 || len > cap) ? 0 : pages_of(len) - pages_of(keep);
+  };
+
+  // With more than one chunk of rows, or many pages, the pages are divided among the
+  // workgroups; a few are moved by the first alone, and the others need not wait for it:
+  // rows that it has shortened already count as nothing to them.
+  uint32_t total = 0;
+  bool alone = gridDim.x == 1;
+  uint32_t next = blockIdx.x * uint32_t(kThreads) + threadIdx.x;
+  uint32_t stride = gridDim.x * uint32_t(kThreads);
+  for (int r0 = 0; r0 < a.batch; r0 += kChunk) {
+    const uint32_t total0 = total;
+    int count[kRowsPerThread];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int at = int(threadIdx.x) * kRowsPerThread + i, r = a.batch - 1 - r0 - at;
+      count[i] = 0;
+      s_end[at] = 0;
+      if (r >= 0) {
+        int len;
+        const int keep = kept(r, len);
+        count[i] = pages_between(keep, len);
+        s_end[at] = pages_of(len);
+      }
+      mine += static_cast<uint32_t>(count[i]);
+    }
+    uint32_t upto = scan_before(mine, total, 0x7fffffffu, s_wave);
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      upto += static_cast<uint32_t>(count[i]);
+      s_upto[int(threadIdx.x) * kRowsPerThread + i] = upto;
+    }
+    __syncthreads();
+    if (a.batch <= kChunk && !alone && total <= kFewPages) {
+      if (blockIdx.x != 0) return;
+      alone = true;
+      next = threadIdx.x;
+      stride = kThreads;
+    }
+    const int rows = min(a.batch - r0, kChunk);
+    for (; next < total; next += stride) {
+      const int at = first_above(s_upto, rows, next);
+      const uint32_t before = at > 0 ? s_upto[at - 1] : total0;
+      const int entry = s_end[at] - 1 - static_cast<int>(next - before);
+      int32_t* from = a.block_table + int64_t(a.batch - 1 - r0 - at) * a.max_pages + entry;
+      const int64_t to = int64_t(free) + next;
+      if (to < a.num_pool_pages) a.free_pages[to] = *from;
+      *from = -1;
+    }
+    __syncthreads();
+  }
+  if (!alone && !last_to_arrive(a.state + kStateArrivals, gridDim.x, &s_last)) return;
+  __syncthreads();
+  for (int r = threadIdx.x; r < a.batch; r += kThreads) {
+    int len;
+    const int keep = kept(r, len);
+    if (keep != len) a.lens[r] = keep;
+  }
+  if (threadIdx.x == 0)
+    a.state[kStateFree] =
+        static_cast<int>(min(int64_t(free) + total, int64_t(a.num_pool_pages)));
+}
+
+}  // namespace
+
+pkv_status launch_take(const TakeArgs& a, hipStream_t s) {
+  const int64_t groups = std::max<int64_t>(1, (int64_t(a.num_tokens) + kTokens - 1) / kTokens);
+  hipLaunchKernelGGL(take_kernel, dim3(static_cast<uint32_t>(groups)), dim3(kThreads), 0, s, a);
+  return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
+}
+
+pkv_status launch_release(const ReleaseArgs& a, hipStream_t s) {
+  const int64_t most = std::min<int64_t>(a.num_pool_pages, int64_t(a.batch) * a.max_pages);
+  const int64_t groups = std::min<int64_t>(64, (most + 2 * kFewPages - 1) / (2 * kFewPages));
+  hipLaunchKernelGGL(release_kernel, dim3(static_cast<uint32_t>(std::max<int64_t>(1, groups))),
+                     dim3(kThreads), 0, s, a);
+  return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
+}
+
+}  // namespace pkv

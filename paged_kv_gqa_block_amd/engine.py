@@ -14,7 +14,7 @@ import os
 import numpy as np
 import torch
 
-from . import _context, _lib
+from . import _context, _lib, _serving
 from ._lib import (PATH_IDS, PATH_NAMES, PKV_NOSPLIT, PKV_WORKQUEUE, make_problem, pkv_decode,
                    pkv_decode_device, pkv_merge, pkv_merge_device, pkv_plan, pkv_plan_bytes,
                    pkv_plan_device, pkv_policy)
@@ -193,7 +193,7 @@ class SelfPlannedStep(_PersistentStepBuffers):
 
 class _ContextCalls:
     """Argument checks and stream choice shared by the context operators
-    (include/pkv_context.h).  They run on the device of their buffers, on the
+    (include/pkv_context.h, include/pkv_serving.h).  They run on the device of their buffers, on the
     given stream or that device's current one.
 
     The first call on a stream waits for the fills of what the object allocated,
@@ -216,11 +216,14 @@ class _ContextCalls:
         self._index = self.device.index
         self.dtype = torch.bfloat16 if prob.dtype == _lib.PKV_BF16 else torch.float16
         self.kv4_page_bytes = _context.pkv_kv4_page_bytes(prob.head_dim)
+        self.kv8_page_bytes = _serving.pkv_kv8_page_bytes(prob.head_dim)
 
         p = prob
         self._shapes = {"block_table": (p.batch, p.max_pages_per_row), "seq_lens": (p.batch,),
                         "tok_offsets": (p.batch + 1,),
                         "kv4_pool": (p.num_pool_pages, p.num_kv_heads, self.kv4_page_bytes),
+                        "kv8_pool": (p.num_pool_pages, p.num_kv_heads, self.kv8_page_bytes),
+                        "kv8_scales": (p.num_pool_pages, p.num_kv_heads, 2),
                         "pool": (p.num_pool_pages, p.num_kv_heads, p.page_size, p.head_dim),
                         "token": (p.num_kv_heads, p.head_dim),
                         "q": (p.batch, p.num_q_heads, p.head_dim)}
@@ -290,13 +293,25 @@ class _ContextCalls:
     def _kv4_pool(self, pool) -> int:
         return self._expect("kv4_pool", pool, self._shapes["kv4_pool"], torch.uint8)
 
+    def _kv8_pool(self, pool, scales) -> tuple:
+        s = self._shapes
+        return (self._expect("kv8_pool", pool, s["kv8_pool"], torch.uint8),
+                self._expect("kv8_scales", scales, s["kv8_scales"], torch.uint8))
+
     def _pools(self, w: dict) -> tuple:
-        """The cache of `w`: (its 4-bit pool,) or (its two 16-bit pools)."""
+        """The cache of `w`: (its 4-bit pool,), (its 8-bit pool, the scales) or (its
+        two 16-bit pools); ``_kind`` says which."""
         if "kv4_pool" in w:
             return (self._kv4_pool(w["kv4_pool"]),)
+        if "kv8_pool" in w:
+            return self._kv8_pool(w["kv8_pool"], w["kv8_scales"])
         shape = self._shapes["pool"]
         return (self._expect("k_pool", w["k_pool"], shape, self.dtype),
                 self._expect("v_pool", w["v_pool"], shape, self.dtype))
+
+    @staticmethod
+    def _kind(w: dict) -> str:
+        return "kv4" if "kv4_pool" in w else "kv8" if "kv8_pool" in w else "window"
 
     def _new_tokens(self, name: str, t: torch.Tensor, n: int) -> tuple:
         """Address and token stride of new keys or values."""
@@ -360,6 +375,50 @@ class Kv4Cache(_ContextCalls):
         return k_out, v_out
 
 
+class Kv8Cache(_ContextCalls):
+    """The paged cache held in 8 bits: K and V of one layer in one byte pool, with
+    a power-of-two scale for each page and KV head of either.
+
+    ``store`` quantises a run of new tokens as it writes them and ``load``
+    reads a run back, as ``Kv4Cache``; ``Kv8Step``, ``PromptStep`` and ``CrossStep``
+    attend over ``pool`` and ``scales``.
+    """
+
+    def __init__(self, prob: _lib.pkv_problem, pool: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, device="cuda"):
+        if (pool is None) != (scales is None):
+            raise ValueError("kv8_pool and kv8_scales go together")
+        super().__init__(prob, pool.device if pool is not None else device)
+        own = pool is None
+        if own:
+            pool, scales = (torch.zeros(self._shapes[n], dtype=torch.uint8, device=self.device)
+                            for n in ("kv8_pool", "kv8_scales"))
+        self._cache = self._kv8_pool(pool, scales)
+        self.pool, self.scales = pool, scales
+        if own:
+            self._own_buffers(pool, scales)
+
+    def store(self, k_new, v_new, block_table, seq_lens, tok_offsets=None, stream=None) -> None:
+        """As ``Kv4Cache.store``.  A page that the run enters behind earlier tokens
+        keeps at least its scale; where that grows, the earlier tokens are rounded
+        again."""
+        n = k_new.shape[0]
+        table, lens = self._tables(block_table, seq_lens)
+        self._launch("pkv_kv8_store", self._offsets(tok_offsets, n), n, lens,
+                     *self._new_tokens("k_new", k_new, n), *self._new_tokens("v_new", v_new, n),
+                     table, *self._cache, self._stream(stream))
+
+    def load(self, block_table, seq_lens, tok_offsets, k_out, v_out, stream=None) -> tuple:
+        """The values the cache stands for, into k_out, v_out [tokens][Hkv][d]."""
+        n = k_out.shape[0]
+        shape = (n, *self._shapes["token"])
+        table, lens = self._tables(block_table, seq_lens)
+        self._launch("pkv_kv8_load", self._offsets(tok_offsets, n), n, lens, table, *self._cache,
+                     self._expect("k_out", k_out, shape, self.dtype),
+                     self._expect("v_out", v_out, shape, self.dtype), self._stream(stream))
+        return k_out, v_out
+
+
 def store_kv(prob: _lib.pkv_problem, k_new, v_new, block_table, seq_lens, tok_offsets, k_pool,
              v_pool, stream=None) -> None:
     """Write a run of new tokens into the 16-bit pools (arguments as
@@ -382,7 +441,7 @@ class WindowStep(_ContextCalls):
     arguments checked and marshalled once, for loops over fixed buffers.
     """
 
-    _call, _num_pools = "pkv_attend_window", 2
+    _call, _takes = "pkv_attend_window", "window"
 
     def __init__(self, prob: _lib.pkv_problem, window: int = 0, sinks: int = 0,
                  splits: int | None = None, device="cuda"):
@@ -409,7 +468,7 @@ class WindowStep(_ContextCalls):
         q = self._expect("q", w["q"], self._shapes["q"], self.dtype)
         table, lens = self._tables(w["block_table"], w["seq_lens"])
         pools = self._pools(w)
-        if len(pools) != self._num_pools:
+        if self._kind(w) != self._takes:
             raise ValueError(f"{type(self).__name__} over the wrong kind of cache")
         return (self._view_ref, lens, self.splits, q, *pools, table, *self._own,
                 self._stream(stream))
@@ -426,16 +485,24 @@ class Kv4Step(WindowStep):
     """One decode step over the 4-bit cache (q, kv4_pool, block_table,
     seq_lens), with the view of ``WindowStep``."""
 
-    _call, _num_pools = "pkv_attend_kv4", 1
+    _call, _takes = "pkv_attend_kv4", "kv4"
+
+
+class Kv8Step(WindowStep):
+    """One decode step over the 8-bit cache (q, kv8_pool, kv8_scales, block_table,
+    seq_lens), with the view of ``WindowStep``."""
+
+    _call, _takes = "pkv_attend_kv8", "kv8"
 
 
 class PromptStep(_ContextCalls):
     """Causal attention of up to `num_tokens` new tokens, all rows together,
-    over a 16-bit or 4-bit cache that already holds them.  Owns the output and
+    over a 16-bit, 4-bit or 8-bit cache that already holds them.  Owns the output and
     the workspace, as ``WindowStep``.
 
     ``run`` takes q [num_tokens][Hq][d], tok_offsets [B + 1] (or None for one
-    token per row), block_table, seq_lens and k_pool, v_pool or kv4_pool.
+    token per row), block_table, seq_lens and k_pool, v_pool or kv4_pool or
+    kv8_pool, kv8_scales.
     """
 
     def __init__(self, prob: _lib.pkv_problem, num_tokens: int, window: int = 0, sinks: int = 0,
@@ -466,7 +533,7 @@ class PromptStep(_ContextCalls):
         q = self._expect("q", w["q"], self.out.shape, self.dtype)
         table, lens = self._tables(w["block_table"], w["seq_lens"])
         pools = self._pools(w)
-        return ("pkv_prompt_kv4" if len(pools) == 1 else "pkv_prompt_window", self._view_ref,
+        return ("pkv_prompt_" + self._kind(w), self._view_ref,
                 self._offsets(w.get("tok_offsets"), n), n, lens, self.splits, q, *pools, table,
                 *self._own,
                 self._stream(stream))
@@ -477,6 +544,106 @@ class PromptStep(_ContextCalls):
     def run_bound(self, bound: tuple) -> tuple:
         self._launch(*bound)
         return self.out, self.lse
+
+
+class CrossStep(_ContextCalls):
+    """Cross attention of up to `num_tokens` queries, all rows together, over the
+    cached states of an encoder: a row's queries see all of its states.  `prob` is
+    the encoder cache's problem.  Owns the output and the workspace, as
+    ``WindowStep``.
+
+    ``run`` takes q [num_tokens][Hq][d], tok_offsets [B + 1] (or None for one query
+    per row), block_table, seq_lens (states of each row) and k_pool, v_pool or
+    kv4_pool or kv8_pool, kv8_scales.
+    """
+
+    _calls = {"window": "pkv_cross", "kv4": "pkv_cross_kv4", "kv8": "pkv_cross_kv8"}
+
+    def __init__(self, prob: _lib.pkv_problem, num_tokens: int, splits: int | None = None,
+                 device="cuda"):
+        super().__init__(prob, device)
+        self.num_tokens = num_tokens
+        ways = (False, True) if num_tokens == prob.batch else (False,)  # with and without offsets
+        if splits is None:
+            cus = torch.cuda.get_device_properties(self.device).multi_processor_count
+            splits = min(_serving.pkv_cross_splits(prob, num_tokens, one, cus) for one in ways)
+        self.splits = splits
+        nbytes = max(_serving.pkv_cross_workspace_bytes(prob, num_tokens, one, splits)
+                     for one in ways)
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
+                               device=self.device)
+        self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
+                               device=self.device)
+        self._own_buffers(self.workspace, self.out, self.lse)
+        self._own = (self.workspace.data_ptr(), nbytes, self.out.data_ptr(), self.lse.data_ptr())
+
+    def bind(self, w: dict, stream=None) -> tuple:
+        n = self.num_tokens
+        q = self._expect("q", w["q"], self.out.shape, self.dtype)
+        table, lens = self._tables(w["block_table"], w["seq_lens"])
+        pools = self._pools(w)
+        return (self._calls[self._kind(w)], self._offsets(w.get("tok_offsets"), n), n, lens,
+                self.splits, q, *pools, table, *self._own, self._stream(stream))
+
+    def run(self, w: dict, stream=None) -> tuple:
+        return self.run_bound(self.bind(w, stream))
+
+    def run_bound(self, bound: tuple) -> tuple:
+        self._launch(*bound)
+        return self.out, self.lse
+
+
+class PageTable(_ContextCalls):
+    """Block table, row lengths and free pages of a cache, kept on the device.
+
+    ``take`` gives a step's new tokens (up to `num_tokens`, all rows together) their
+    pages and returns what the step's calls read; ``release`` cuts rows down and
+    takes their pages back.  Every page starts out free and every row empty; to start
+    elsewhere, fill ``block_table``, ``lens``, ``free_pages`` and ``state[0]``, the
+    number of free pages.  ``state[1]`` counts the rows that the last ``take`` turned
+    down.  Calls change the tables in place, one after the other.
+    """
+
+    def __init__(self, prob: _lib.pkv_problem, num_tokens: int, device="cuda"):
+        super().__init__(prob, device)
+        if num_tokens < 0:
+            raise ValueError(f"{num_tokens} tokens")
+        self.num_tokens = num_tokens
+        p, i32 = prob, {"dtype": torch.int32, "device": self.device}
+        self.block_table = torch.full((p.batch, p.max_pages_per_row), -1, **i32)
+        self.lens = torch.zeros(p.batch, **i32)
+        self.free_pages = torch.arange(p.num_pool_pages - 1, -1, -1, **i32)  # page 0 on top
+        self.state = torch.zeros(4, **i32)
+        self.state[0].fill_(p.num_pool_pages)
+        self.seq_lens = torch.zeros(p.batch, **i32)
+        self.tok_offsets = torch.zeros(p.batch + 1, **i32)
+        self.slots = torch.full((num_tokens,), -1, dtype=torch.int64, device=self.device)
+        self.positions = torch.full((num_tokens,), -1, **i32)
+        self._own_buffers(self.block_table, self.lens, self.free_pages, self.state, self.seq_lens,
+                          self.tok_offsets, self.slots, self.positions)
+        self._step = {"block_table": self.block_table, "seq_lens": self.seq_lens,
+                      "tok_offsets": self.tok_offsets, "slots": self.slots,
+                      "positions": self.positions}
+        self._take = tuple(t.data_ptr() for t in (
+            self.lens, self.block_table, self.free_pages, self.state, self.seq_lens,
+            self.tok_offsets, self.slots, self.positions))
+
+    def take(self, counts, stream=None) -> dict:
+        """Pages for counts [B] new tokens of every row.  Returns the object's buffers
+        block_table, seq_lens (0 for a row turned down), tok_offsets, slots and
+        positions (-1 for its tokens), which the next call overwrites."""
+        self._launch("pkv_pages_take",
+                     self._expect("counts", counts, self._shapes["seq_lens"], torch.int32),
+                     self.num_tokens, *self._take, self._stream(stream))
+        return dict(self._step)
+
+    def release(self, keep, stream=None) -> None:
+        """Cut rows down to keep [B] tokens: 0 ends a row, a negative number or the
+        row's length and more leaves it alone."""
+        self._launch("pkv_pages_release",
+                     self._expect("keep", keep, self._shapes["seq_lens"], torch.int32),
+                     *self._take[:4], self._stream(stream))
 
 
 def load_policy_table(path: str = POLICY_TABLE_PATH):
