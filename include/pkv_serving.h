@@ -70,8 +70,13 @@ pkv_status pkv_kv8_load(const pkv_problem* prob, const int32_t* tok_offsets, int
 
 /*
  * Decode and prompt attention over the 8-bit cache: pkv_attend_kv4 and
- * pkv_prompt_kv4 (arguments, split caps, workspaces, errors) with the scales beside
- * the pool.
+ * pkv_prompt_kv4 with the scales beside the pool.  Decode has their split caps
+ * and workspaces too.  A prompt's max_splits is the number of workgroups of a KV head
+ * that its tiles are spread over, by even shares of all the work there is, whatever
+ * tiles that cuts (1: a workgroup for each tile; no more than fill the current
+ * device, and of 8 steps of 64 keys or more each).  pkv_prompt_kv8_splits and
+ * pkv_prompt_kv8_workspace_bytes give its caps and workspaces, on the terms of
+ * pkv_prompt_splits and pkv_prompt_workspace_bytes.
  */
 pkv_status pkv_attend_kv8(const pkv_problem* prob, const pkv_view* view,
                           const int32_t* seq_lens_dev, int32_t max_splits, const void* q,
@@ -85,6 +90,11 @@ pkv_status pkv_prompt_kv8(const pkv_problem* prob, const pkv_view* view,
                           const int32_t* block_table, void* workspace, size_t workspace_bytes,
                           void* out, float* lse, hipStream_t stream);
 
+size_t pkv_prompt_kv8_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
+                                      int32_t one_per_row, int32_t max_splits);
+int32_t pkv_prompt_kv8_splits(const pkv_problem* prob, const pkv_view* view, int32_t num_tokens,
+                              int32_t one_per_row, int32_t num_cus);
+
 /*
  * Cross attention of num_tokens queries, ragged over the rows as tok_offsets says
  * (NULL: one per row, num_tokens = B), over 16-bit pages, the 4-bit or the 8-bit
@@ -93,9 +103,9 @@ pkv_status pkv_prompt_kv8(const pkv_problem* prob, const pkv_view* view,
  *   Calls of few queries a row (by num_tokens, B and G alone) keep 16 or more bits of
  *   a weight in the second product, as decode does; calls of many round it to the
  *   problem's type, as prompts do.  Statistics and sums are held in fp32.
- *   max_splits: a tile of queries cuts its keys into up to this many ranges;
- *     pkv_cross_splits gives a cap that fills num_cus compute units (0 on an invalid
- *     argument).
+ *   max_splits: few queries: a tile cuts its keys into up to this many ranges; many:
+ *     as pkv_prompt_kv8's.  pkv_cross_splits gives a cap that fills num_cus compute
+ *     units (0 on an invalid argument).
  *   workspace: pkv_cross_workspace_bytes device bytes (0 for one split and where
  *     the call would be refused), on the terms of pkv_attend_window's; one_per_row
  *     says that the call passes no tok_offsets.

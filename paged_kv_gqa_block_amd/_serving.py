@@ -9,7 +9,8 @@ from ._context import _byref, token_stride
 from ._lib import LIB, _check, _ptr, _stream, pkv_problem
 
 EXPORTED = ("pkv_kv8_page_bytes", "pkv_kv8_store", "pkv_kv8_load", "pkv_attend_kv8",
-            "pkv_prompt_kv8", "pkv_cross_workspace_bytes", "pkv_cross_splits", "pkv_cross",
+            "pkv_prompt_kv8", "pkv_prompt_kv8_workspace_bytes", "pkv_prompt_kv8_splits",
+            "pkv_cross_workspace_bytes", "pkv_cross_splits", "pkv_cross",
             "pkv_cross_kv4", "pkv_cross_kv8", "pkv_pages_take", "pkv_pages_release")
 
 
@@ -23,6 +24,8 @@ def _prototypes() -> None:
             ("pkv_attend_kv8", i32, [prob, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp, vp]),
             ("pkv_prompt_kv8", i32,
              [prob, vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp, vp]),
+            ("pkv_prompt_kv8_workspace_bytes", sz, [prob, i32, i32, i32]),
+            ("pkv_prompt_kv8_splits", i32, [prob, vp, i32, i32, i32]),
             ("pkv_cross_workspace_bytes", sz, [prob, i32, i32, i32]),
             ("pkv_cross_splits", i32, [prob, i32, i32, i32]),
             ("pkv_cross", i32, [prob, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp, vp]),
@@ -78,6 +81,17 @@ def pkv_prompt_kv8(prob, view, tok_offsets, num_tokens: int, seq_lens_dev, max_s
         ctypes.byref(prob), _byref(view), _ptr(tok_offsets), num_tokens, _ptr(seq_lens_dev),
         max_splits, _ptr(q), _ptr(kv8_pool), _ptr(kv8_scales), _ptr(block_table),
         *_workspace(workspace), _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def pkv_prompt_kv8_workspace_bytes(prob, num_tokens: int, one_per_row: bool,
+                                   max_splits: int) -> int:
+    return LIB.pkv_prompt_kv8_workspace_bytes(ctypes.byref(prob), num_tokens, one_per_row,
+                                              max_splits)
+
+
+def pkv_prompt_kv8_splits(prob, view, num_tokens: int, one_per_row: bool, num_cus: int) -> int:
+    return LIB.pkv_prompt_kv8_splits(ctypes.byref(prob), _byref(view), num_tokens, one_per_row,
+                                     num_cus)
 
 
 def pkv_cross_workspace_bytes(prob, num_tokens: int, one_per_row: bool, max_splits: int) -> int:

@@ -27,7 +27,8 @@ SOURCES = [
     "append.hip", "cost_model.cpp", "noalloc.hip", "noalloc_api.cpp",
     "context/context_api.cpp", "context/attend.hip", "context/kv4_cache.hip", "context/prompt.hip",
     "serving/serving_api.cpp", "serving/kv8_cache.hip", "serving/kv8_attend.hip",
-    "serving/kv8_prompt.hip", "serving/cross_few.hip", "serving/cross_many.hip", "serving/pages.hip",
+    "serving/kv8_prompt.hip", "serving/cross_few.hip", "serving/cross_many.hip",
+    "serving/pages.hip",
 ]
 PROBE_SOURCES = ["read_probe.hip"]
 

@@ -22,7 +22,8 @@ pkv_status prompt(const pkv_problem* prob, const pkv_view* view, const int32_t* 
                   size_t workspace_bytes, void* out, float* lse, hipStream_t stream) {
   PromptArgs a;
   const pkv_status st = fill_prompt(prob, view, tok_offsets, num_tokens, seq_lens, max_splits, q,
-                                    pools, block_table, workspace, workspace_bytes, out, lse, &a);
+                                    pools, block_table, workspace, workspace_bytes, out, lse,
+                                    Divide::kRanges, &a);
   if (st != PKV_OK || a.num_tokens == 0) return st;
   return launch_prompt(*prob, pools.kind == Cache::k4, a, stream);
 }
@@ -171,11 +172,7 @@ extern "C" pkv_status pkv_prompt_kv4(const pkv_problem* prob, const pkv_view* vi
 
 extern "C" size_t pkv_prompt_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
                                              int32_t one_per_row, int32_t max_splits) {
-  const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
-  if (tiles < 0 || max_splits < 2 || max_splits > 65535 ||
-      !prompt_fits(prob, tiles, max_splits))
-    return 0;
-  return prompt_workspace_of(prob, tiles, max_splits);
+  return prompt_bytes(prob, tiles_of(prob, num_tokens, one_per_row), max_splits, Divide::kRanges);
 }
 
 extern "C" int32_t pkv_prompt_splits(const pkv_problem* prob, const pkv_view* view,

@@ -151,14 +151,22 @@ inline pkv_status fill_attend(const pkv_problem* prob, const pkv_view* view,
   return PKV_OK;
 }
 
+// How the tiles of a prompt are divided: each into up to max_splits ranges, or all of a KV
+// head's into max_splits even shares (serving/shares.h).
+enum class Divide { kRanges, kShares };
+
 // Launch size of a prompt, and its counters where it is split.
-inline bool prompt_fits(const pkv_problem* p, int64_t tiles, int32_t splits) {
+inline bool prompt_fits(const pkv_problem* p, int64_t tiles, int32_t splits, Divide by) {
   const int64_t pairs = tiles * p->num_kv_heads;
-  return pairs * splits <= kMaxGridGroups && (splits == 1 || pairs <= kCounters);
+  const int64_t parts = by == Divide::kShares ? (tiles + splits - 1) * p->num_kv_heads
+                                              : pairs * splits;
+  return parts <= kMaxGridGroups && (splits == 1 || pairs <= kCounters);
 }
 
-inline size_t prompt_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits) {
-  return kCounterBytes + static_cast<size_t>(tiles) * p->num_kv_heads * splits *
+// Shares: a part of a tile has the state tile + share, and no two of them the same.
+inline size_t prompt_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits, Divide by) {
+  const int64_t states = by == Divide::kShares ? tiles + splits - 1 : tiles * splits;
+  return kCounterBytes + static_cast<size_t>(states) * p->num_kv_heads *
                              prompt_state_floats(p->head_dim) * sizeof(float);
 }
 
@@ -168,7 +176,8 @@ inline pkv_status fill_prompt(const pkv_problem* prob, const pkv_view* view,
                               const int32_t* tok_offsets, int32_t num_tokens,
                               const int32_t* seq_lens, int32_t max_splits, const void* q,
                               Pools pools, const int32_t* block_table, void* workspace,
-                              size_t workspace_bytes, void* out, float* lse, PromptArgs* args) {
+                              size_t workspace_bytes, void* out, float* lse, Divide by,
+                              PromptArgs* args) {
   PromptArgs& a = *args;
   a = PromptArgs{};
   pkv_status st = check_run(prob, tok_offsets, num_tokens, seq_lens, block_table);
@@ -203,13 +212,20 @@ inline pkv_status fill_prompt(const pkv_problem* prob, const pkv_view* view,
   a.tile_pages = static_cast<int32_t>(
       std::min<int64_t>(most_pages(prob, view) + kTileRows / a.group / 16 + 2, a.max_pages));
   const int64_t tiles = prompt_tiles(a);
-  if (!prompt_fits(prob, tiles, max_splits)) return PKV_ERANGE;
+  if (!prompt_fits(prob, tiles, max_splits, by)) return PKV_ERANGE;
   if (max_splits > 1) {
-    if (workspace_bytes < prompt_workspace_of(prob, tiles, max_splits)) return PKV_ENOSPC;
+    if (workspace_bytes < prompt_workspace_of(prob, tiles, max_splits, by)) return PKV_ENOSPC;
     a.arrivals = static_cast<int32_t*>(workspace);
     a.state = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
   }
   return PKV_OK;
+}
+
+// pkv_prompt_workspace_bytes and its like.
+inline size_t prompt_bytes(const pkv_problem* p, int64_t tiles, int32_t max_splits, Divide by) {
+  if (tiles < 0 || max_splits < 2 || max_splits > 65535 || !prompt_fits(p, tiles, max_splits, by))
+    return 0;
+  return prompt_workspace_of(p, tiles, max_splits, by);
 }
 
 // Query tiles of a run batch, from the host's numbers alone; -1 when invalid.

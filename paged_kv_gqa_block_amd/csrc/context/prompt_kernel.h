@@ -49,6 +49,7 @@
 #include "context/runs.h"
 #include "context/states.h"
 #include "serving/kv8_common.h"
+#include "serving/shares.h"
 
 namespace pkv {
 
@@ -83,31 +84,54 @@ __device__ __forceinline__ uint2 read_transposed(const void* p) {
                                        (lds_bf16x4*)(lds_void*)(const_cast<void*>(p))));
 }
 
-template <int D, bool BF16, Cache F, bool CROSS>
-__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles, int slots) {
+// One of equal ranges of a tile's steps (find_tile).
+struct SplitPart {
+  int item;   // of the tile among those that the launch lists
+  int split, splits;
+  int steps;  // of a range at least
+};
+
+// A share's part of a tile: [from, to) of its cost on the line, the parts of other shares
+// ending at multiples of `each`.  In LDS, a copy for each wave: its registers are needed
+// for the tile.
+struct LinePart {
+  int64_t start, cost, slot;  // as in SharePart
+  int64_t from, to, each, end;
+  __device__ __forceinline__ int step_at(int64_t v, int all_steps) const {
+    return __builtin_amdgcn_readfirstlane(
+        static_cast<int>(static_cast<double>(min(max(v, int64_t(0)), cost)) * all_steps /
+                         static_cast<double>(cost)));
+  }
+};
+
+// A tile of a run, or a part of its steps.  Part: SplitPart or LinePart.
+template <int D, bool BF16, Cache F, bool CROSS, typename Part>
+__device__ __forceinline__ void prompt_tile(const PromptArgs& a, int g, const Run& run, int k_tile,
+                                            const Part& part, uint4 (&kt0)[kKeys][D / 8],
+                                            uint4 (&kt1)[kKeys][D / 8], uint4 (&vt0)[kKeys][D / 8],
+                                            uint4 (&vt1)[kKeys][D / 8], bool* s_last) {
+  constexpr bool kLine = std::is_same_v<Part, LinePart>;
   constexpr bool KV4 = F == Cache::k4, KV8 = F == Cache::k8;
+  // 16-bit pages: scores and weights in one stretch of code, in the order that the
+  // groups below set.  A launch of few workgroups takes 4 % less (chunks of 36 tokens 72.6
+  // and 69.6 us); a full one is bound by power, not by cycles, and takes the same.
+  // (With a page's registers between, 4 and 8 bits took 2-4 % more.)
+  constexpr bool kInterleave = F == Cache::k16 && D == 128;
+  constexpr int kVector = 0x402, kMfma = 0x008, kDsRead = 0x100;  // classes of instructions
   constexpr int NQ = D / 16;   // products over the channels
   constexpr int NC = D / 32;   // channel blocks of the output
   constexpr int CH = D / 8;    // 16-byte chunks of a key
   constexpr int KPL = 64 / CH; // keys of one 1 KiB load
   constexpr int NL = 16 / KPL; // loads of a page
-  // Objects of their own, named at compile time where they are used: the
-  // compiler then knows which loads to LDS a read has to wait for.
   using Tile = uint4[kKeys][CH];
-  __shared__ Tile kt0, kt1, vt0, vt1;
-  __shared__ bool s_last;
-  const int tid = threadIdx.x, lane = tid & 63;
+  int thread = threadIdx.x;
+  // New to every tile: what depends on it alone, kept over the loop of a share's tiles,
+  // spilled.
+  if constexpr (kLine) asm volatile("" : "+v"(thread));
+  const int tid = thread, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
-  const int g = blockIdx.x % a.num_kv_heads;
-  const int ts = blockIdx.x / a.num_kv_heads;
   const int G = a.group;
-
-  const TileRun found = find_tile(a, ts, tiles, slots);
-  const int k_tile = found.tile, splits = found.splits;
-  if (k_tile < 0) return;
-  const Run& run = found.run;
-  const int item = ts / splits, split = ts - item * splits;
   const int64_t rows64 = int64_t(run.count) * G;
   if (int64_t(k_tile) * kTileRows >= rows64) return;
   const int r0 = k_tile * kTileRows;
@@ -134,7 +158,10 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   const bool mine = my < rows;
 
   if (p_last < 0) {  // no query of the tile is at a position of the row
-    if (mine && split == 0) {
+    bool writes;
+    if constexpr (kLine) writes = part.from == 0;
+    else writes = part.split == 0;
+    if (mine && writes) {
       for (int e = h; e < D / 4; e += 2)
         reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qh * D)[e] = make_uint2(0u, 0u);
       if (a.lse && h == 0) a.lse[qh] = kNegInf;
@@ -144,9 +171,19 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
   const int window = a.window > 0 ? a.window : 0x7fffffff;
   const SeenPages sp = seen_pages(p_first, p_last, a.window, a.sinks);
   const int all_steps = (sp.count + 3) >> 2;
-  const int per_split = max(found.steps, (all_steps + splits - 1) / splits);
-  const int s_begin = split * per_split, s_end = min(s_begin + per_split, all_steps);
-  if (s_begin >= s_end) return;
+  int s_begin, s_end, per_split = 0;
+  if constexpr (kLine) {
+    s_begin = part.step_at(part.from, all_steps), s_end = part.step_at(part.to, all_steps);
+  } else {
+    per_split = max(part.steps, (all_steps + part.splits - 1) / part.splits);
+    s_begin = part.split * per_split, s_end = min(s_begin + per_split, all_steps);
+  }
+  // A part of a cut tile may be too short for a step: it leaves a state of nothing.
+  if constexpr (kLine) {
+    if (all_steps == 0 || (s_begin >= s_end && part.to - part.from == part.cost)) return;
+  } else {
+    if (s_begin >= s_end) return;
+  }
   const int32_t* bt = a.block_table + int64_t(run.row) * a.max_pages;
 
   // Steps whose every key is seen by every query of the wave (absent pages
@@ -352,7 +389,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
     }
   };
   const int kq = (lane & 15) >> 2, cq = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  auto softmax_pv = [&](const Tile& vt, const f32x16 (&s)[2]) __attribute__((always_inline)) {
+  // The running maximum of the query, moved where a step's scores pass it.
+  auto raise = [&](const f32x16 (&s)[2]) __attribute__((always_inline)) {
     float t0 = max3(s[0][0], s[1][0], s[1][0]), t1 = max3(s[0][1], s[1][1], s[1][1]);
 #pragma unroll
     for (int i = 2; i < 16; i += 2) {
@@ -370,6 +408,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
         for (int i = 0; i < 16; ++i) acc[cb][i] *= alpha;
       m_run = mn;
     }
+  };
+  auto weigh = [&](const Tile& vt, const f32x16 (&s)[2]) __attribute__((always_inline)) {
     uint32_t pb[2][8];
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub)
@@ -379,6 +419,8 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
         const float e1 = fast_exp2(fmaf(s[sub][2 * i + 1], a.scale_log2, -m_run));
         pb[sub][i] = pack2<BF16>(e0, e1);
         l_part += e0 + e1;
+        // The sum with the weights: left to the step's end, it kept all of them.
+        if constexpr (kInterleave) asm("" : "+v"(pb[sub][i]), "+v"(l_part));
       }
     // Lane's share of a transposed read: key lane % 16 / 4 of four, 16-byte
     // chunk 2 (lane / 16 % 2) + lane % 4 / 2 of a channel block, half lane % 2.
@@ -427,6 +469,7 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
     if constexpr (KV8) r.scales = __builtin_amdgcn_readlane(scales, at + wave);
     return r;
   };
+  if (!kLine || s_begin < s_end) {
   StepPages pg0 = pages_of(s_begin), pg1 = pages_of(s_begin + 1);
   issue_k(pg0.id, s_begin, kt0);
   issue_v(pg0.id, s_begin, vt0);
@@ -453,6 +496,12 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
       issue_k(pg2.id, s + 2, k_cur);
       issue_v(pg1.id, s + 1, v_next);
     }
+    const bool full = (s >= full_lo && s < full_hi) || s < sink_hi;
+    auto settle = [&] {
+      if (!full || pg0.bad) mask(s, pg0.bad, sc);
+      raise(sc);
+    };
+    if constexpr (kInterleave) settle();
     scores(k_next, sn);
     if constexpr (KV4) {  // to registers: later, so that fewer are taken meanwhile
       issue_k(pg2.id, s + 2, k_cur);
@@ -462,9 +511,24 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
       put_v(v_next, pg1.scales);
       issue_k(pg2.id, s + 2, k_cur);
     }
-    const bool full = (s >= full_lo && s < full_hi) || s < sink_hi;
-    if (!full || pg0.bad) mask(s, pg0.bad, sc);
-    softmax_pv(v_cur, sc);
+    if constexpr (!kInterleave) settle();
+    weigh(v_cur, sc);
+    if constexpr (kInterleave) {
+      // Between two products of the next scores: an LDS read four products ahead and a
+      // share of this step's weights (32 exponentials, 80 other instructions).
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * NQ; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kVector, 112 / (2 * NQ), 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * NC; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
+      }
+    }
     put_k(k_cur, pg2.scales);
     if constexpr (!KV8) put_v(v_next, 0u);
     if constexpr (KV8) issue_v(pg2.id, s + 2, v_cur);
@@ -477,54 +541,80 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
     step(s, kt0, kt1, vt0, vt1, sa, sb);
     if (s + 1 < s_end) step(s + 1, kt1, kt0, vt1, vt0, sb, sa);
   }
+  }
 
   // ---- outputs ----------------------------------------------------------------
   float l = sum_x32(l_part);
-  const int ns = (all_steps + per_split - 1) / per_split;
-  if (ns > 1) {
-    // State of a split: [d / 2 pairs][thread][2] of O and [thread][2] of m, l.
-    const int64_t tg = int64_t(item) * a.num_kv_heads + g;
+  bool whole;
+  if constexpr (kLine) whole = part.to - part.from == part.cost;
+  else whole = per_split >= all_steps;
+  if (!whole) {
+    // State of a part: [d / 2 pairs][thread][2] of O and [thread][2] of m, l.
     constexpr int64_t kSlot = 256 * (D / 2 + 2);
-    float* mine_st = a.state + (tg * a.splits + split) * kSlot;
+    int64_t tg, slot0, slot1;      // tile and KV head; slots of a part of it and of the next
+    int mine_at, first_at = 0, last_at;  // parts: this one, and those of the tile
+    if constexpr (kLine) {
+      tg = part.slot * a.num_kv_heads + g;
+      slot0 = tg, slot1 = tg + a.num_kv_heads;
+      mine_at = static_cast<int>((part.start + part.from) / part.each);
+      first_at = static_cast<int>(part.start / part.each);
+      last_at = static_cast<int>((part.start + part.cost - 1) / part.each);
+    } else {
+      tg = int64_t(part.item) * a.num_kv_heads + g;
+      slot0 = tg * a.splits, slot1 = slot0 + 1;
+      mine_at = part.split, last_at = (all_steps + per_split - 1) / per_split - 1;
+    }
+    const float* st0 = a.state + slot0 * kSlot;
+    const int64_t next = (slot1 - slot0) * kSlot;
+    float* mine_st = a.state + slot0 * kSlot + mine_at * next;
 #pragma unroll
     for (int cb = 0; cb < NC; ++cb)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         put_state(mine_st + ((cb * 8 + i) * 256 + tid) * 2, acc[cb][2 * i], acc[cb][2 * i + 1]);
     put_state(mine_st + (NC * 8 * 256 + tid) * 2, m_run, l);
-    if (!last_to_arrive(arrival_counter(a.arrivals, tg), ns, &s_last)) return;
-    // Joined in split order, so that the result does not depend on the order
+    if (!last_to_arrive(arrival_counter(a.arrivals, tg), last_at - first_at + 1, s_last)) return;
+    // Joined in order, so that the result does not depend on the order
     // of arrival: first the maximum, then the weighted sums.
-    const float* st0 = a.state + tg * a.splits * kSlot;
-    constexpr int U = 8;  // splits whose m and l are under way together
+    constexpr int U = 8;  // parts whose m and l are under way together
     auto get_ml = [&](int s) {
-      return get_state2(st0 + min(s, ns - 1) * kSlot + (NC * 8 * 256 + tid) * 2);
+      return get_state2(st0 + min(s, last_at) * next + (NC * 8 * 256 + tid) * 2);
     };
     m_run = kLowest;
-    for (int s0 = 0; s0 < ns; s0 += U) {
+    for (int s0 = first_at; s0 <= last_at; s0 += U) {
       float2 ml[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) ml[u] = get_ml(s0 + u);
 #pragma unroll
-      for (int u = 0; u < U; ++u) m_run = fmaxf(m_run, ml[u].x);
+      for (int u = 0; u < U; ++u)
+        m_run = fmaxf(m_run, ml[u].x);
     }
     l = 0.f;
 #pragma unroll
     for (int cb = 0; cb < NC; ++cb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[cb][i] = 0.f;
-    for (int s = 0; s < ns; ++s) {
-      const float* st = st0 + s * kSlot;
+    for (int s = first_at; s <= last_at; ++s) {
+      const float* st = st0 + s * next;
       const float2 ml = get_ml(s);
+      // All of a state on its way at once: one load after the other took 7 us a state.
+      float2 o[NC][8];
+#pragma unroll
+      for (int cb = 0; cb < NC; ++cb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[cb][i] = get_state2(st + ((cb * 8 + i) * 256 + tid) * 2);
+#pragma unroll
+      for (int cb = 0; cb < NC; ++cb)
+        asm volatile("" : "+v"(o[cb][0].x), "+v"(o[cb][1].x), "+v"(o[cb][2].x), "+v"(o[cb][3].x),
+                          "+v"(o[cb][4].x), "+v"(o[cb][5].x), "+v"(o[cb][6].x), "+v"(o[cb][7].x));
       const float w = fast_exp2(ml.x - m_run);
       l = fmaf(w, ml.y, l);
 #pragma unroll
       for (int cb = 0; cb < NC; ++cb)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 o = get_state2(st + ((cb * 8 + i) * 256 + tid) * 2);
-          acc[cb][2 * i] = fmaf(w, o.x, acc[cb][2 * i]);
-          acc[cb][2 * i + 1] = fmaf(w, o.y, acc[cb][2 * i + 1]);
+          acc[cb][2 * i] = fmaf(w, o[cb][i].x, acc[cb][2 * i]);
+          acc[cb][2 * i + 1] = fmaf(w, o[cb][i].y, acc[cb][2 * i + 1]);
         }
     }
   }
@@ -543,18 +633,77 @@ __global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles,
 }
 
 template <int D, bool BF16, Cache F, bool CROSS>
+__global__ __launch_bounds__(256, 2) void prompt_kernel(PromptArgs a, int tiles, int slots) {
+  // Objects of their own, named at compile time where they are used: the
+  // compiler then knows which loads to LDS a read has to wait for.
+  __shared__ uint4 kt0[kKeys][D / 8], kt1[kKeys][D / 8], vt0[kKeys][D / 8], vt1[kKeys][D / 8];
+  __shared__ bool s_last;
+  const int g = blockIdx.x % a.num_kv_heads;
+  const int ts = blockIdx.x / a.num_kv_heads;
+  const TileRun found = find_tile<CROSS>(a, ts, tiles, slots);
+  if (found.tile < 0) return;
+  SplitPart part{ts / found.splits, 0, found.splits, found.steps};
+  part.split = ts - part.item * found.splits;
+  prompt_tile<D, BF16, F, CROSS>(a, g, found.run, found.tile, part, kt0, kt1, vt0, vt1, &s_last);
+}
+
+// The same in even shares: workgroup i of a KV head takes [i each, (i + 1) each) of the
+// line of its tiles (serving/shares.h).
+template <int D, bool BF16, Cache F, bool CROSS>
+__global__ __launch_bounds__(256, 2) void prompt_shares_kernel(PromptArgs a, int slots) {
+  __shared__ uint4 kt0[kKeys][D / 8], kt1[kKeys][D / 8], vt0[kKeys][D / 8], vt1[kKeys][D / 8];
+  __shared__ bool s_last;
+  __shared__ LinePart s_part[4];
+  const int g = blockIdx.x % a.num_kv_heads;
+  const int share = blockIdx.x / a.num_kv_heads;
+  LinePart& part = s_part[threadIdx.x >> 6];
+  Shares shares;
+  int64_t at;
+  SharePart p = find_part<CROSS>(a, share, slots, at, shares);
+  if (p.cost == 0) return;
+  part.each = shares.each;
+  part.end = min(shares.total, at + shares.each);
+  for (;;) {
+    part.start = p.start, part.cost = p.cost, part.slot = p.slot;
+    part.from = at - p.start;
+    part.to = min(p.cost, part.end - p.start);
+    prompt_tile<D, BF16, F, CROSS>(a, g, p.run, p.tile, part, kt0, kt1, vt0, vt1, &s_last);
+    at = readlane64(part.start + part.to, 0);
+    if (at >= readlane64(part.end, 0)) return;
+    p = find_part<CROSS>(a, -1, slots, at, shares);
+    if (p.cost == 0) return;
+  }
+}
+
+// Workgroups a KV head that run at the same time: two a compute unit.
+inline int prompt_slots(int cus, int num_kv_heads) { return 2 * cus / num_kv_heads; }
+
+template <int D, bool BF16, Cache F, bool CROSS>
 inline pkv_status launch_prompt_kernel(const PromptArgs& a, hipStream_t s) {
   const int64_t tiles = prompt_tiles(a);
-  // Workgroups a KV head that run at the same time: two a compute unit.
   int slots = 0;
   if (a.splits > 1) {
     const int cus = current_compute_units();
     if (cus <= 0) return PKV_EHIP;
-    slots = 2 * cus / a.num_kv_heads;
+    slots = prompt_slots(cus, a.num_kv_heads);
   }
   hipLaunchKernelGGL((prompt_kernel<D, BF16, F, CROSS>),
                      dim3(static_cast<uint32_t>(tiles * a.num_kv_heads * a.splits)), dim3(256), 0,
                      s, a, static_cast<int>(tiles), slots);
+  return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
+}
+
+// One workgroup a tile, or with more than one split in even shares.
+template <int D, bool BF16, Cache F, bool CROSS>
+inline pkv_status launch_prompt_shares(const PromptArgs& a, hipStream_t s) {
+  if (a.splits == 1) return launch_prompt_kernel<D, BF16, F, CROSS>(a, s);
+  const int cus = current_compute_units();
+  if (cus <= 0) return PKV_EHIP;
+  const int slots = std::max(prompt_slots(cus, a.num_kv_heads), 1);
+  // Whole tiles: a workgroup each.
+  const int64_t n = std::max<int64_t>(std::min(a.splits, slots), prompt_tiles(a));
+  hipLaunchKernelGGL((prompt_shares_kernel<D, BF16, F, CROSS>),
+                     dim3(static_cast<uint32_t>(n * a.num_kv_heads)), dim3(256), 0, s, a, slots);
   return hipGetLastError() == hipSuccess ? PKV_OK : PKV_EHIP;
 }
 

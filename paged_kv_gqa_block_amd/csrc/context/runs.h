@@ -75,7 +75,9 @@ struct TileRun {
 // counted first, so that tiles times ranges fill `slots` workgroups a KV head
 // and no more, and no more ranges than the longest row's steps are worth; a shorter
 // tile's ranges are as long as the longest one's.
-template <typename Args>
+// LONGEST: up to 64 rows are taken in the order of their lengths, the longest first, for
+// tiles that cost what their row is long: launched last, a long one would end alone.
+template <bool LONGEST = false, typename Args>
 __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, int slots) {
   const int lane = threadIdx.x & 63;
   TileRun t;
@@ -91,7 +93,7 @@ __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, i
     }
     return t;
   }
-  int first, next, len, count;
+  int first, next, len, count, row_of_lane = lane;
   auto load = [&](int r0) {  // 64 rows from r0 on; count: tiles up to and with a lane's row
     const int r = r0 + lane;
     first = a.tok_offsets[min(r, a.batch)];
@@ -99,6 +101,19 @@ __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, i
     len = a.seq_lens[min(r, a.batch - 1)];
     asm volatile("" : "+v"(first), "+v"(next), "+v"(len));  // one wait for the three
     first = clamp_offset(first, a.num_tokens), next = clamp_offset(next, a.num_tokens);
+    if (LONGEST && a.batch <= 64) {
+      const int key = r < a.batch ? clean_len(len, a.max_pages) : -1;
+      int rank = 0;
+      for (int k = 0; k < a.batch; ++k) {
+        const int other = __builtin_amdgcn_readlane(key, k);
+        rank += other > key || (other == key && k < lane) ? 1 : 0;
+      }
+      rank = r < a.batch ? rank : lane;
+      first = __builtin_amdgcn_ds_permute(rank << 2, first);
+      next = __builtin_amdgcn_ds_permute(rank << 2, next);
+      len = __builtin_amdgcn_ds_permute(rank << 2, len);
+      row_of_lane = __builtin_amdgcn_ds_permute(rank << 2, lane);
+    }
     const int64_t rows = int64_t(max(next - first, 0)) * a.group;
     count = wave_scan(r < a.batch ? static_cast<int>((rows + kTileRows - 1) / kTileRows) : 0);
   };
@@ -126,7 +141,8 @@ __device__ __forceinline__ TileRun find_tile(const Args& a, int ts, int tiles, i
     if (item < before + in_all) {
       const uint64_t past = __builtin_amdgcn_ballot_w64(before + count > item);
       const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(past));
-      t.run = make_run(r0 + at, __builtin_amdgcn_readlane(first, at),
+      const int row = LONGEST ? __builtin_amdgcn_readlane(row_of_lane, at) : at;
+      t.run = make_run(r0 + row, __builtin_amdgcn_readlane(first, at),
                        __builtin_amdgcn_readlane(next, at), __builtin_amdgcn_readlane(len, at),
                        a.max_pages);
       t.tile = before + __builtin_amdgcn_readlane(count, at) - 1 - item;

@@ -8,9 +8,9 @@ namespace {
 template <int D, bool BF16>
 pkv_status launch_kind(Cache kind, const PromptArgs& a, hipStream_t s) {
   switch (kind) {
-    case Cache::k16: return launch_prompt_kernel<D, BF16, Cache::k16, true>(a, s);
-    case Cache::k4: return launch_prompt_kernel<D, BF16, Cache::k4, true>(a, s);
-    default: return launch_prompt_kernel<D, BF16, Cache::k8, true>(a, s);
+    case Cache::k16: return launch_prompt_shares<D, BF16, Cache::k16, true>(a, s);
+    case Cache::k4: return launch_prompt_shares<D, BF16, Cache::k4, true>(a, s);
+    default: return launch_prompt_shares<D, BF16, Cache::k8, true>(a, s);
   }
 }
 

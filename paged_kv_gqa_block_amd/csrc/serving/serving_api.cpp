@@ -97,9 +97,44 @@ extern "C" pkv_status pkv_prompt_kv8(const pkv_problem* prob, const pkv_view* vi
   const pkv_status st =
       fill_prompt(prob, view, tok_offsets, num_tokens, seq_lens_dev, max_splits, q,
                   {Cache::k8, kv8_pool, nullptr, kv8_scales}, block_table, workspace,
-                  workspace_bytes, out, lse, &a);
+                  workspace_bytes, out, lse, Divide::kShares, &a);
   if (st != PKV_OK || a.num_tokens == 0) return st;
   return launch_prompt8(*prob, a, stream);
+}
+
+namespace {
+
+// Shares a KV head of tiles of 128 queries: as many workgroups as run at once, as long as
+// they get eight steps each.  Where the tiles alone may be as many, they stay whole:
+// the tiles of a row then walk its keys together and read them out of the L2 (8 rows of
+// 1024-8192 states, 97 tiles for 64 workgroups, 16 bits: 306 us whole, 326 in shares;
+// 24 tiles for 64, 8 bits, 3000-31000 states: 582 whole, 258 in shares).  A prompt, or
+// cross attention (view null: every query sees the whole table).
+int32_t shares_for(const pkv_problem* p, const pkv_view* view, int32_t num_tokens, int64_t tiles,
+                   int32_t num_cus) {
+  const int64_t slots = std::max<int64_t>(2 * int64_t(num_cus) / p->num_kv_heads, 1);
+  const int64_t pages = std::min<int64_t>(most_pages(p, view) + ceil_div(num_tokens, 16),
+                                          p->max_pages_per_row);
+  const int64_t shares = std::min(slots, tiles * (ceil_div(pages, 4) / kRangeSteps));
+  if (tiles > slots || shares < 2 ||
+      !prompt_fits(p, tiles, static_cast<int32_t>(shares), Divide::kShares))
+    return 1;
+  return static_cast<int32_t>(shares);
+}
+
+}  // namespace
+
+extern "C" size_t pkv_prompt_kv8_workspace_bytes(const pkv_problem* prob, int32_t num_tokens,
+                                                 int32_t one_per_row, int32_t max_splits) {
+  return prompt_bytes(prob, tiles_of(prob, num_tokens, one_per_row), max_splits, Divide::kShares);
+}
+
+extern "C" int32_t pkv_prompt_kv8_splits(const pkv_problem* prob, const pkv_view* view,
+                                         int32_t num_tokens, int32_t one_per_row,
+                                         int32_t num_cus) {
+  const int64_t tiles = tiles_of(prob, num_tokens, one_per_row);
+  if (tiles < 0 || check_view(view) != PKV_OK || num_cus < 1 || num_cus > 1024) return 0;
+  return num_tokens == 0 ? 1 : shares_for(prob, view, num_tokens, tiles, num_cus);
 }
 
 // ---- cross attention -------------------------------------------------------------
@@ -133,7 +168,7 @@ pkv_status cross(const pkv_problem* prob, const int32_t* tok_offsets, int32_t nu
     PromptArgs a;
     const pkv_status st = fill_prompt(prob, nullptr, tok_offsets, num_tokens, seq_lens, max_splits,
                                       q, pools, block_table, workspace, workspace_bytes, out, lse,
-                                      &a);
+                                      Divide::kShares, &a);
     if (st != PKV_OK || a.num_tokens == 0) return st;
     return launch_cross_many(*prob, pools.kind, a, stream);
   }
@@ -180,7 +215,7 @@ extern "C" size_t pkv_cross_workspace_bytes(const pkv_problem* prob, int32_t num
   if (tiles_of(prob, num_tokens, one_per_row) < 0 || max_splits < 2 || max_splits > 65535)
     return 0;
   if (!cross_takes_few(*prob, num_tokens, one_per_row != 0))
-    return pkv_prompt_workspace_bytes(prob, num_tokens, one_per_row, max_splits);
+    return pkv_prompt_kv8_workspace_bytes(prob, num_tokens, one_per_row, max_splits);
   const int64_t tiles = cross_tiles(*prob, num_tokens, one_per_row != 0);
   return cross_fits(prob, tiles, max_splits) ? cross_workspace_of(prob, tiles, max_splits).bytes
                                              : 0;
@@ -191,7 +226,7 @@ extern "C" int32_t pkv_cross_splits(const pkv_problem* prob, int32_t num_tokens,
   if (tiles_of(prob, num_tokens, one_per_row) < 0 || num_cus < 1 || num_cus > 1024) return 0;
   if (num_tokens == 0) return 1;
   if (!cross_takes_few(*prob, num_tokens, one_per_row != 0))
-    return pkv_prompt_splits(prob, nullptr, num_tokens, one_per_row, num_cus);
+    return pkv_prompt_kv8_splits(prob, nullptr, num_tokens, one_per_row, num_cus);
   // The launch counts the real tiles; there are at least these.
   const int64_t rows = int64_t(num_tokens) * (prob->num_q_heads / prob->num_kv_heads);
   const int64_t likely = std::max(ceil_div(rows, kCrossRows),

@@ -431,6 +431,13 @@ def store_kv(prob: _lib.pkv_problem, k_new, v_new, block_table, seq_lens, tok_of
                   calls._stream(stream))
 
 
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace of the attention calls: its counters, the first 256 KiB, are zero."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256 << 10].zero_()
+    return ws
+
+
 class WindowStep(_ContextCalls):
     """One decode step over the visible part of a 16-bit cache: the last
     `window` tokens (0: all) and the first `sinks`.
@@ -510,16 +517,18 @@ class PromptStep(_ContextCalls):
         super().__init__(prob, device)
         self.view = _context.make_view(window, sinks)
         self.num_tokens = num_tokens
+        self.splits = self.splits8 = splits
         if splits is None:
-            splits = _context.pkv_prompt_splits(
-                prob, self.view, num_tokens, False, torch.cuda.get_device_properties(
-                    self.device).multi_processor_count)
-        self.splits = splits
-        nbytes = _context.pkv_prompt_workspace_bytes(prob, num_tokens, False, splits)
-        if num_tokens == prob.batch:  # room for calls without tok_offsets too
-            nbytes = max(nbytes, _context.pkv_prompt_workspace_bytes(prob, num_tokens, True,
-                                                                     splits))
-        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            cus = torch.cuda.get_device_properties(self.device).multi_processor_count
+            self.splits = _context.pkv_prompt_splits(prob, self.view, num_tokens, False, cus)
+            self.splits8 = _serving.pkv_prompt_kv8_splits(prob, self.view, num_tokens, False, cus)
+        # Room for calls over every kind of cache, and without tok_offsets too.
+        ways = (False, True) if num_tokens == prob.batch else (False,)
+        nbytes = max(max(_context.pkv_prompt_workspace_bytes(prob, num_tokens, one, self.splits),
+                         _serving.pkv_prompt_kv8_workspace_bytes(prob, num_tokens, one,
+                                                                 self.splits8))
+                     for one in ways)
+        self.workspace = _workspace(nbytes, self.device)
         self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
                                device=self.device)
         self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,
@@ -532,11 +541,10 @@ class PromptStep(_ContextCalls):
         n = self.num_tokens
         q = self._expect("q", w["q"], self.out.shape, self.dtype)
         table, lens = self._tables(w["block_table"], w["seq_lens"])
-        pools = self._pools(w)
-        return ("pkv_prompt_" + self._kind(w), self._view_ref,
-                self._offsets(w.get("tok_offsets"), n), n, lens, self.splits, q, *pools, table,
-                *self._own,
-                self._stream(stream))
+        pools, kind = self._pools(w), self._kind(w)
+        return ("pkv_prompt_" + kind, self._view_ref, self._offsets(w.get("tok_offsets"), n), n,
+                lens, self.splits8 if kind == "kv8" else self.splits, q, *pools, table,
+                *self._own, self._stream(stream))
 
     def run(self, w: dict, stream=None) -> tuple:
         return self.run_bound(self.bind(w, stream))
@@ -570,7 +578,7 @@ class CrossStep(_ContextCalls):
         self.splits = splits
         nbytes = max(_serving.pkv_cross_workspace_bytes(prob, num_tokens, one, splits)
                      for one in ways)
-        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.workspace = _workspace(nbytes, self.device)
         self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
                                device=self.device)
         self.lse = torch.empty(num_tokens, prob.num_q_heads, dtype=torch.float32,

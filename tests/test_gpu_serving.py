@@ -374,6 +374,63 @@ def test_prompt_splits(splits):
         assert _same(first, step.out)
 
 
+# Tiles of uneven cost in even shares: rows of 1 to 94 steps, some of one token, one empty.
+UNEVEN = ([6000, 40, 900, 0, 300], [70, 40, 100, 5, 33])
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1000, 3)])
+def test_prompt_in_shares(window, sinks, d, dtype):
+    lens, new = UNEVEN
+    b = Batch8(71, lens, new, hkv=2, group=4, d=d, dtype=dtype, window=window, sinks=sinks)
+    ref, w = b.reference(), b.device()
+    for splits in (None, 2, 3, 5, 9, 40):
+        say(f"[kv8 shares] W={window} d={d} {dtype} splits={splits}")
+        step = engine.PromptStep(b.problem(), int(b.new.sum()), window, sinks, splits)
+        for _ in range(2):  # on one workspace, with the same bits
+            out, lse = step.run(w)
+            torch.cuda.synchronize()
+            check(out, lse, ref, dtype, d, b.vmax, True, f"splits {splits}")
+            first = out.clone() if _ == 0 else first
+        assert _same(first, out) and not step.workspace[:256 << 10].any()
+
+
+@pytest.mark.parametrize("kind", [16, 4, 8])
+@pytest.mark.parametrize("d,dtype", [(128, "f16"), (64, "bf16")])
+def test_cross_in_shares(d, dtype, kind):
+    lens, queries = UNEVEN
+    b = make_cross(kind, 72, lens, queries, hkv=2, group=4, d=d, dtype=dtype)
+    ref, w = cross_reference(b), b.device()
+    for splits in (None, 2, 3, 5, 9, 40, 200):
+        say(f"[cross shares] d={d} {dtype} bits={kind} splits={splits}")
+        step = engine.CrossStep(b.problem(), int(b.new.sum()), splits)
+        out, lse = step.run(w)
+        torch.cuda.synchronize()
+        check(out, lse, ref, dtype, d, b.vmax, True, f"splits {splits}")
+        assert not step.workspace[:256 << 10].any()
+
+
+def test_shares_over_many_rows():
+    """More rows than a wave holds, one of them long; prompts and cross attention."""
+    rng = np.random.default_rng(9)
+    lens = rng.integers(0, 60, 90)
+    lens[77] = 4000
+    new = np.minimum(lens, rng.integers(0, 50, 90))
+    new[77] = 130
+    n = int(new.sum())
+    for splits in (None, 6):
+        say(f"[shares, rows] splits={splits}")
+        b = Batch8(73, lens, new, hkv=1, group=3, d=64)
+        step = engine.PromptStep(b.problem(), n, splits=splits)
+        out, lse = step.run(b.device())
+        torch.cuda.synchronize()
+        check(out, lse, b.reference(), "f16", 64, b.vmax, True, "prompt")
+        b = make_cross(8, 74, lens, new, hkv=1, group=3, d=64)
+        out, lse = engine.CrossStep(b.problem(), n, splits).run(b.device())
+        torch.cuda.synchronize()
+        check(out, lse, cross_reference(b), "f16", 64, b.vmax, True, "cross")
+
+
 def test_prompt_outside_the_row_and_behind_the_last():
     """Runs longer than their rows, invalid lengths, pages outside the pool; output
     rows behind the last offset stay as they were."""

@@ -130,6 +130,27 @@ def test_prompt_refusals():
     assert _prompt(n=0) == PKV_OK
 
 
+def test_prompt_shares():
+    """Caps and workspaces of a prompt's even shares, over the whole range."""
+    from paged_kv_gqa_block_amd import _context
+    ws, sp = _serving.pkv_prompt_kv8_workspace_bytes, _serving.pkv_prompt_kv8_splits
+    for b in (1, 2, 65, 65535):
+        for hq, hkv in ((1, 1), (16, 1), (8, 8), (64, 8), (4096, 4096)):
+            for pages in (1, 41, 2048, (2 ** 31 - 1) // 16):
+                p = _prob(batch=b, num_q_heads=hq, num_kv_heads=hkv, max_pages_per_row=pages)
+                for view in (None, _context.make_view(1, 0), _context.make_view(2 ** 31 - 1, 5)):
+                    for n in (0, 1, 2, 129, 5000, 10 ** 6):
+                        s = sp(p, view, n, False, 256)
+                        assert 1 <= s <= 512 and (s == 1 or ws(p, n, False, s) > 0)
+                    assert sp(p, view, b, True, 256) >= 1
+    p = _prob(max_pages_per_row=2048)
+    state = 256 * (128 // 2 + 2) * 4
+    assert ws(p, 10, False, 3) == (256 << 10) + (2 + 3 - 1) * 2 * state
+    assert ws(p, 2, True, 3) == (256 << 10) + (2 + 3 - 1) * 2 * state
+    assert ws(p, 10, False, 1) == 0 and ws(p, 3, True, 3) == 0 and ws(p, -1, False, 3) == 0
+    assert sp(p, None, 10, False, 0) == 0 and sp(p, _context.make_view(-1, 0), 10, False, 256) == 0
+
+
 def _cross(kind, prob=None, off=P, n=10, lens=P, splits=1, q=P, k=P, v=P, bt=P, ws=None,
            ws_bytes=0, out=P):
     head = (ctypes.byref(prob or _prob()), off, n, lens, splits, q)
