@@ -16,7 +16,7 @@ void launch_kind(Cache kind, int64_t tiles, const AttendArgs& a, hipStream_t s) 
     hipLaunchKernelGGL((attend_kernel<D, BF16, Cache::k4, true, 16, 4, 2, 2>), grid, dim3(256), 0,
                        s, a);
   else
-    hipLaunchKernelGGL((attend_kernel<D, BF16, Cache::k8, true, 16, 4, 2, 1>), grid, dim3(256), 0,
+    hipLaunchKernelGGL((attend_kernel<D, BF16, Cache::k8, true, 16, 4, 1, 2>), grid, dim3(256), 0,
                        s, a);
 }
 

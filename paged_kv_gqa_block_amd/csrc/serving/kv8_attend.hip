@@ -8,7 +8,7 @@ namespace {
 template <int D, bool BF16, int GP>
 void launch_one(const AttendArgs& a, hipStream_t s) {
   const dim3 grid(a.num_kv_heads, a.splits, a.batch);
-  hipLaunchKernelGGL((attend_kernel<D, BF16, Cache::k8, false, GP, 4, 2, 1>), grid, dim3(256), 0,
+  hipLaunchKernelGGL((attend_kernel<D, BF16, Cache::k8, false, GP, 4, 1, 2>), grid, dim3(256), 0,
                      s, a);
 }
 

@@ -92,102 +92,113 @@ __global__ __launch_bounds__(kThreads) void take_kernel(TakeArgs a) {
   const uint32_t most = static_cast<uint32_t>(a.num_tokens) + 1;
   const uint32_t begin = blockIdx.x * uint32_t(kTokens), end = begin + kTokens;
   const int free = free_count(a.state, a.num_pool_pages);
-  bool finish = gridDim.x == 1;  // this workgroup writes the rows' results
+  uint32_t tokens = 0, asked = 0, granted = 0, denied = 0;
+  // One chunk of rows, four a thread.
+  int cnt[kRowsPerThread], len[kRowsPerThread], need[kRowsPerThread];
+  uint32_t upto[kRowsPerThread];
+  bool ok[kRowsPerThread];
+  auto scan = [&](int r0) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int r = r0 + int(threadIdx.x) * kRowsPerThread + i;
+      cnt[i] = r < a.batch ? max(a.counts[r], 0) : 0;
+      len[i] = r < a.batch ? a.lens[r] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i)
+      mine = min(mine + min(static_cast<uint32_t>(cnt[i]), most), most);
+    uint32_t before = scan_before(mine, tokens, most, s_wave);
+    uint32_t wants = 0;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      s_off[int(threadIdx.x) * kRowsPerThread + i] = before;
+      upto[i] = before = min(before + min(static_cast<uint32_t>(cnt[i]), most), most);
+      ok[i] = len[i] >= 0 && len[i] <= cap && cnt[i] <= cap - len[i] && upto[i] < most;
+      need[i] = ok[i] ? pages_of(len[i] + cnt[i]) - pages_of(len[i]) : 0;
+      wants += static_cast<uint32_t>(need[i]);
+    }
+    uint32_t rank = scan_before(wants, asked, 0x7fffffffu, s_wave);
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int at = int(threadIdx.x) * kRowsPerThread + i;
+      ok[i] = ok[i] && (need[i] == 0 || rank + need[i] <= static_cast<uint32_t>(free));
+      s_upto[at] = upto[i];
+      s_rank[at] = rank;
+      s_len[at] = ok[i] ? len[i] : -1;
+      rank += static_cast<uint32_t>(need[i]);
+    }
+  };
+  auto write_rows = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int r = r0 + int(threadIdx.x) * kRowsPerThread + i;
+      if (r >= a.batch) break;
+      if (ok[i]) granted += static_cast<uint32_t>(need[i]);
+      if (!ok[i] && cnt[i] > 0) ++denied;
+      a.seq_lens[r] = ok[i] ? len[i] + cnt[i] : 0;
+      a.tok_offsets[r + 1] = static_cast<int>(min(upto[i], most - 1));
+      if (ok[i]) a.lens[r] = len[i] + cnt[i];
+    }
+  };
 
-  for (int pass = 0; pass < 2; ++pass) {
-    uint32_t tokens = 0, asked = 0, granted = 0, denied = 0;
-    for (int r0 = 0; r0 < a.batch; r0 += kChunk) {
-      const uint32_t tokens0 = tokens;
-      int cnt[kRowsPerThread], len[kRowsPerThread];
-      uint32_t mine = 0;
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        const int r = r0 + int(threadIdx.x) * kRowsPerThread + i;
-        cnt[i] = r < a.batch ? max(a.counts[r], 0) : 0;
-        len[i] = r < a.batch ? a.lens[r] : 0;
-      }
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i)
-        mine = min(mine + min(static_cast<uint32_t>(cnt[i]), most), most);
-      uint32_t before = scan_before(mine, tokens, most, s_wave);
-      uint32_t off[kRowsPerThread], upto[kRowsPerThread];
-      int need[kRowsPerThread];
-      bool ok[kRowsPerThread];
-      uint32_t wants = 0;
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        off[i] = before;
-        upto[i] = before = min(before + min(static_cast<uint32_t>(cnt[i]), most), most);
-        ok[i] = len[i] >= 0 && len[i] <= cap && cnt[i] <= cap - len[i] && upto[i] < most;
-        need[i] = ok[i] ? pages_of(len[i] + cnt[i]) - pages_of(len[i]) : 0;
-        wants += static_cast<uint32_t>(need[i]);
-      }
-      uint32_t rank = scan_before(wants, asked, 0x7fffffffu, s_wave);
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        const int at = int(threadIdx.x) * kRowsPerThread + i, r = r0 + at;
-        ok[i] = ok[i] && (need[i] == 0 || rank + need[i] <= static_cast<uint32_t>(free));
-        s_upto[at] = upto[i];
-        s_off[at] = off[i];
-        s_rank[at] = rank;
-        s_len[at] = ok[i] ? len[i] : -1;
-        rank += static_cast<uint32_t>(need[i]);
-        if (ok[i]) granted += static_cast<uint32_t>(need[i]);
-        if (r < a.batch && !ok[i] && cnt[i] > 0) ++denied;
-        if (finish && r < a.batch) {
-          a.seq_lens[r] = ok[i] ? len[i] + cnt[i] : 0;
-          a.tok_offsets[r + 1] = static_cast<int>(min(upto[i], most - 1));
-          if (ok[i]) a.lens[r] = len[i] + cnt[i];
+  const bool single = gridDim.x == 1;
+  for (int r0 = 0; r0 < a.batch; r0 += kChunk) {
+    const uint32_t tokens0 = tokens;
+    scan(r0);
+    __syncthreads();
+    const int rows = min(a.batch - r0, kChunk);
+    const uint32_t stop = min(min(tokens, most - 1), end);
+    for (uint32_t t = begin + threadIdx.x; t < stop; t += kThreads) {
+      if (t < tokens0) continue;
+      const int at = first_above(s_upto, rows, t);
+      const int held = s_len[at];
+      int64_t slot = -1;
+      int p = -1;
+      if (held >= 0) {
+        const int64_t row = int64_t(r0 + at) * a.max_pages;
+        p = held + static_cast<int>(t - s_off[at]);
+        const int entry = p >> 4, had = pages_of(held);
+        int page;
+        if (entry >= had) {
+          page = a.free_pages[free - 1 - static_cast<int>(s_rank[at]) - (entry - had)];
+          if ((p & 15) == 0) a.block_table[row + entry] = page;
+        } else {
+          page = a.block_table[row + entry];
         }
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pool_pages))
+          slot = int64_t(page) * 16 + (p & 15);
       }
-      __syncthreads();
-      if (pass == 0) {
-        const int rows = min(a.batch - r0, kChunk);
-        const uint32_t stop = min(min(tokens, most - 1), end);
-        for (uint32_t t = begin + threadIdx.x; t < stop; t += kThreads) {
-          if (t < tokens0) continue;
-          const int at = first_above(s_upto, rows, t);
-          const int held = s_len[at];
-          int64_t slot = -1;
-          int p = -1;
-          if (held >= 0) {
-            const int64_t row = int64_t(r0 + at) * a.max_pages;
-            p = held + static_cast<int>(t - s_off[at]);
-            const int entry = p >> 4, had = pages_of(held);
-            int page;
-            if (entry >= had) {
-              page = a.free_pages[free - 1 - static_cast<int>(s_rank[at]) - (entry - had)];
-              if ((p & 15) == 0) a.block_table[row + entry] = page;
-            } else {
-              page = a.block_table[row + entry];
-            }
-            if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pool_pages))
-              slot = int64_t(page) * 16 + (p & 15);
-          }
-          if (a.slots) a.slots[t] = slot;
-          if (a.positions) a.positions[t] = p;
-        }
-        if (!finish && tokens >= end) break;  // the rows behind have none of its tokens
-      }
+      if (a.slots) a.slots[t] = slot;
+      if (a.positions) a.positions[t] = p;
     }
-    if (finish) {
-      const uint32_t all = static_cast<uint32_t>(wave_sum_i(static_cast<int>(granted)));
-      const uint32_t no = static_cast<uint32_t>(wave_sum_i(static_cast<int>(denied)));
-      __shared__ uint32_t s_all[4], s_no[4];
-      if ((threadIdx.x & 63) == 0) {
-        s_all[threadIdx.x >> 6] = all;
-        s_no[threadIdx.x >> 6] = no;
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        a.tok_offsets[0] = 0;
-        a.state[kStateFree] = free - static_cast<int>(s_all[0] + s_all[1] + s_all[2] + s_all[3]);
-        a.state[kStateDenied] = static_cast<int>(s_no[0] + s_no[1] + s_no[2] + s_no[3]);
-      }
-      return;
-    }
+    if (single) write_rows(r0);
+    else if (tokens >= end) break;  // the rows behind have none of its tokens
+  }
+  if (!single) {
     if (!last_to_arrive(a.state + kStateArrivals, gridDim.x, &s_last)) return;
-    finish = true;
+    if (a.batch <= kChunk) {
+      write_rows(0);  // as scanned
+    } else {
+      tokens = asked = 0;
+      for (int r0 = 0; r0 < a.batch; r0 += kChunk) {
+        scan(r0);
+        write_rows(r0);
+      }
+    }
+  }
+  const uint32_t all = static_cast<uint32_t>(wave_sum_i(static_cast<int>(granted)));
+  const uint32_t no = static_cast<uint32_t>(wave_sum_i(static_cast<int>(denied)));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    s_wave[threadIdx.x >> 6] = all;
+    s_rank[threadIdx.x >> 6] = no;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.tok_offsets[0] = 0;
+    a.state[kStateFree] = free - static_cast<int>(s_wave[0] + s_wave[1] + s_wave[2] + s_wave[3]);
+    a.state[kStateDenied] = static_cast<int>(s_rank[0] + s_rank[1] + s_rank[2] + s_rank[3]);
   }
 }
 
