@@ -270,12 +270,13 @@ class _ContextCalls:
 
     def _expect(self, name: str, t: torch.Tensor, shape: tuple, dtype) -> int:
         """The address of `t`, after its checks."""
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == self._index
+                and t.is_contiguous()):
+            return t.data_ptr()
         if t.shape != shape or t.dtype != dtype or t.device != self.device:
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} "
                              f"{dtype} on {self.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous")
 
     def _tables(self, block_table, seq_lens) -> tuple:
         s = self._shapes
@@ -316,7 +317,8 @@ class _ContextCalls:
     def _new_tokens(self, name: str, t: torch.Tensor, n: int) -> tuple:
         """Address and token stride of new keys or values."""
         heads, d = self._shapes["token"]
-        if t.shape != (n, heads, d) or t.dtype != self.dtype or t.device != self.device:
+        if (t.dtype is not self.dtype or t.shape != (n, heads, d)
+                or t.get_device() != self._index):
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
         stride = t.stride()
         if n > 1 and stride[1] == d and stride[2] == 1:

@@ -650,9 +650,11 @@ def test_workspace_of_all_shapes():
     a = make_cross(8, 1, [900, 77], [3, 2], hkv=2, group=4)
     c = make_cross(16, 2, [1500, 600, 8], [100, 1, 30], hkv=1, group=8, d=64)
     e = Batch8(3, [2000, 50, 300], hkv=2, group=4)
+    p = Batch8(4, [2100, 60], [30, 20], hkv=2, group=4)
     steps = [(engine.CrossStep(a.problem(), 5, 6), a.device(), cross_reference(a), a, False),
              (engine.CrossStep(c.problem(), 131, 4), c.device(), cross_reference(c), c, True),
-             (engine.Kv8Step(e.problem(), splits=9), e.device(), e.reference(), e, False)]
+             (engine.Kv8Step(e.problem(), splits=9), e.device(), e.reference(), e, False),
+             (engine.PromptStep(p.problem(), 50, splits=7), p.device(), p.reference(), p, True)]
     ws = torch.zeros(max(s.workspace.numel() for s, *_ in steps), dtype=torch.uint8, device="cuda")
     for s, *_ in steps:
         s._own = (ws.data_ptr(), ws.numel(), *s._own[2:])
@@ -707,7 +709,8 @@ def _check_take(t, ref, counts, num_tokens, got):
 @pytest.mark.parametrize("rows,most,num_tokens", [(1, 3, 3), (3, 40, 100), (7, 1, 7), (64, 1, 64),
                                                   (65, 30, 700), (300, 20, 4000),
                                                   (1023, 2, 1500), (1030, 4, 512),
-                                                  (2100, 3, 9000), (4, 5000, 14000)])
+                                                  (2100, 3, 9000), (4, 5000, 14000),
+                                                  (16, 3, 20000), (1024, 1, 3000)])
 def test_page_tables_follow_the_oracle(rows, most, num_tokens):
     """Steps of any counts, rows cut down and ended, lists that run short; one
     workgroup and several, rows beyond one scan."""
@@ -877,6 +880,32 @@ def test_requests_from_start_to_end():
             ref.release(keep)
             _check_table(pages, ref)
     assert ref.lens[0] == 61 and ref.lens[3] == 11  # row 3's 90 tokens had no pages
+
+
+def test_offsets_outside_the_arrays():
+    """Offsets below zero and behind the last token are taken as the arrays' ends: by
+    stores, prompts and cross attention of either kind."""
+    lens, new = [40, 25, 60], [10, 5, 12]
+    off = _i32([-7, 10, 15, 99])
+    say("[offsets outside]")
+    b = Batch8(61, lens, new, hkv=2, group=4, everything=True)
+    w = dict(b.device(), tok_offsets=off)
+    out, lse = engine.PromptStep(b.problem(), 27).run(w)
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "f16", 128, b.vmax, True, "prompt")
+    for queries in (new, [1, 2, 3]):
+        c = make_cross(8, 62, lens, queries)
+        n = sum(queries)
+        bad = _i32([-1, queries[0], queries[0] + queries[1], n + 5])
+        out, lse = engine.CrossStep(c.problem(), n).run(dict(c.device(), tok_offsets=bad))
+        torch.cuda.synchronize()
+        check(out, lse, cross_reference(c), "f16", 128, c.vmax, not _takes_few(c), "cross")
+    caches = [engine.Kv8Cache(b.problem()) for _ in range(2)]
+    kv = torch.randn(27, 2, 2, 128, generator=torch.Generator().manual_seed(3)).half().cuda()
+    for cache, o in zip(caches, (off, _offsets(new))):
+        cache.store(kv[:, 0], kv[:, 1], w["block_table"], w["seq_lens"], o)
+    torch.cuda.synchronize()
+    assert _same(caches[0].pool, caches[1].pool) and _same(caches[0].scales, caches[1].scales)
 
 
 def test_graph_replays():
