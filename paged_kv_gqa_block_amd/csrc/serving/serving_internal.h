@@ -45,9 +45,6 @@ struct ReleaseArgs {
   int32_t num_pool_pages;
 };
 
-// Queries of a row up to which cross attention takes tiles of sixteen.
-constexpr int kFewQueries = 32;
-
 // Tiles of sixteen queries: a bound that needs only the token count.
 inline int64_t cross_tiles(const pkv_problem& p, int32_t num_tokens, bool one_per_row) {
   return one_per_row ? p.batch
@@ -55,10 +52,16 @@ inline int64_t cross_tiles(const pkv_problem& p, int32_t num_tokens, bool one_pe
 }
 
 // Whether a cross-attention call takes tiles of sixteen queries (attend_kernel.h)
-// rather than of 128 (prompt_kernel.h): by the average of its rows' packed queries.
+// rather than of 128 (prompt_kernel.h): up to 32 packed queries a row on the average, 64
+// where few pairs of row and KV head leave room for more tiles.
+//  us, tiles of sixteen / of 128, d = 128, 16 bits: 16 rows x 8 KV heads of 3000-4000
+//  states, 16 queries each 43 / 64, 32 62 / 64, 48 88 / 65 (8 bits: 35 / 57 at 32, 49 / 57
+//  at 48); 8 rows, 32 queries 31 / 52, 64 49 / 52, 96 73 / 53; one row of 20000, 64 queries
+//  53 / 59, 96 73 / 59.  64 rows of 500-8000 in 8 bits: 16 queries 110 / 185, 32 192 / 185.
 inline bool cross_takes_few(const pkv_problem& p, int32_t num_tokens, bool one_per_row) {
   const int64_t rows = int64_t(num_tokens) * (p.num_q_heads / p.num_kv_heads);
-  return rows <= int64_t(kFewQueries) * p.batch && cross_tiles(p, num_tokens, one_per_row) <= 65535;
+  const int64_t few = int64_t(p.batch) * p.num_kv_heads <= 64 ? 64 : 32;
+  return rows <= few * p.batch && cross_tiles(p, num_tokens, one_per_row) <= 65535;
 }
 
 pkv_status launch_attend8(const pkv_problem& p, const AttendArgs& a, hipStream_t s);

@@ -528,8 +528,13 @@ CROSS = [
 
 
 def _takes_few(b):
-    """Whether the call takes tiles of sixteen queries: by the average alone."""
-    return int(b.new.sum()) * b.group <= 32 * len(b.lens)
+    """Whether the call takes tiles of sixteen queries: by the average alone, and more
+    where pairs of row and KV head are few."""
+    return _few(int(b.new.sum()) * b.group, len(b.lens), b.hkv)
+
+
+def _few(queries, rows, hkv):
+    return queries <= (64 if rows * hkv <= 64 else 32) * rows
 
 
 @pytest.mark.parametrize("kind", [16, 4, 8])
@@ -872,7 +877,7 @@ def test_requests_from_start_to_end():
                 if m:
                     ek, ev = enc.kv[r]
                     want = sv.cross_row(q64, ek, ev, enc.scale)
-                    few = n * group <= 32 * rows
+                    few = _few(n * group, rows, hkv)
                     check(c_out[got], c_lse[got], want, dtype, d, enc.vmax, not few, f"cross {r}")
                 at += m
             pages.release(_i32(keep))
