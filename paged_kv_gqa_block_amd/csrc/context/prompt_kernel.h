@@ -150,6 +150,7 @@ __device__ __forceinline__ void prompt_tile(const PromptArgs& a, int g, const Ru
 
   // This lane's query.
   const int wr = 32 * wave;  // the wave's first row in the tile
+  const bool busy = wr < rows;  // else the wave's results are nobody's: no states of O
   const int my = wr + n;
   const int j = token_of(min(my, rows - 1));
   const int head = (r0 + min(my, rows - 1)) - j * G;
@@ -567,13 +568,16 @@ __device__ __forceinline__ void prompt_tile(const PromptArgs& a, int g, const Ru
     const float* st0 = a.state + slot0 * kSlot;
     const int64_t next = (slot1 - slot0) * kSlot;
     float* mine_st = a.state + slot0 * kSlot + mine_at * next;
+    if (busy) {
 #pragma unroll
-    for (int cb = 0; cb < NC; ++cb)
+      for (int cb = 0; cb < NC; ++cb)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        put_state(mine_st + ((cb * 8 + i) * 256 + tid) * 2, acc[cb][2 * i], acc[cb][2 * i + 1]);
+        for (int i = 0; i < 8; ++i)
+          put_state(mine_st + ((cb * 8 + i) * 256 + tid) * 2, acc[cb][2 * i], acc[cb][2 * i + 1]);
+    }  // (16 new tokens behind 32768, 64 rows of 128: 114 us with the states of all, 94 so)
     put_state(mine_st + (NC * 8 * 256 + tid) * 2, m_run, l);
     if (!last_to_arrive(arrival_counter(a.arrivals, tg), last_at - first_at + 1, s_last)) return;
+    if (!busy) return;
     // Joined in order, so that the result does not depend on the order
     // of arrival: first the maximum, then the weighted sums.
     constexpr int U = 8;  // parts whose m and l are under way together
