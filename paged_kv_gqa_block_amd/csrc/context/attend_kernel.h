@@ -176,9 +176,18 @@ __device__ __forceinline__ CrossShare find_cross_share(const AttendArgs& a, int 
     t_max = wave_max(t_max);
     total = __builtin_amdgcn_readlane(wave_scan(total), 63);
     const int pairs = max(total, 1) * a.num_kv_heads;
-    const int most = min(a.splits, decode_ranges(t_max, (a.cus + pairs - 1) / pairs,
-                                                 20 * a.cus / pairs));
-    s.pages = max(1, (t_max + most - 1) / most);
+    const int fill = (a.cus + pairs - 1) / pairs;
+    auto cut = [&](int fill) {
+      const int most = min(a.splits, decode_ranges(t_max, fill, 20 * a.cus / pairs));
+      s.pages = max(1, (t_max + most - 1) / most);
+    };
+    cut(fill);
+    // A few ranges more than compute units: one less each, where each has three and more
+    // (four rows of 3000-4000 states, 48 queries each: 35 -> 27 us).
+    if (fill > 2 && a.batch <= 64) {
+      const int items = wave_scan(tiles * max(1, (pages + s.pages - 1) / s.pages));
+      if (__builtin_amdgcn_readlane(items, 63) * a.num_kv_heads > a.cus) cut(fill - 1);
+    }
   }
   for (int r0 = 0, before = 0;;) {
     const int ranges = max(1, pages / s.pages + (pages % s.pages ? 1 : 0));
