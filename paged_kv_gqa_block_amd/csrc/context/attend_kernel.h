@@ -28,6 +28,15 @@
 // took 18.1 us with a second launch and 17.0 us so, and the host one call less
 // (16 -> 9 us); with 16 states on their way at once 15.8 us.
 //
+// 8 bits, the same 64 rows, 1.05 million tokens (2.15 GB): 356-359 us, 6.0 TB/s; one row
+// of 32768 (67 MB) 17.7, 8192 11.1; eight, half of them short 41 (5.1 TB/s); d = 64 105 us
+// for 587 MB.  Units of one page, three on their way, and of two pages, two on their way,
+// are within 1 % of each other at the large sizes and 4 % apart at the small ones; two
+// pages, three on their way, spill (393 us).
+// CROSS: four queries of 16 rows of 200-1500 states, 16 heads, d = 64, 16 bits (56 MB): 16 us;
+// 1-4 of 64 rows of 500-8000, G = 4, 8 bits (579 MB): 112-114 us, 5.1 TB/s; one to four of
+// 16 rows of 3000-4000, 16 bits (229 MB): 40-43 us.
+//
 // Measured (G = 8, d = 128, 64 rows, 8 KV heads, bf16): 4 bits, 1.1 million
 // tokens (1.21 GB): 212-227 us, 5.3-5.7 TB/s; the same pages read and not used take
 // 187 us (6.5 TB/s), the rest is conversion and matrix work that three waves do

@@ -28,17 +28,23 @@
 // own rounding); maxima, sums (of the unrounded ones) and outputs are fp32 until the
 // last rounding.
 //
-// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096: 402-420 us
-// for 413 GFLOP, card by card, 0.98-1.03 PFLOP/s, 0.82-0.85 of what a square product
-// of 8192 reaches (over 4 bits: 409 us beside 408).  Matrix work fills half of a
-// SIMD's cycles and vector work (exponentials, maxima, rounding) 47 %, and the two
-// hardly overlap.  Direct loads and two scores in flight brought it from 502 us;
-// deeper rings of buffers, pages touched ahead in L2 (430 us), wave priorities and
-// tiles of 64 rows brought nothing.  Eight chunks of 9-54 tokens behind a window of
-// 4096, 64 heads over 8: 65-69 us (4 bits: 67), of which 46 at the same rate, 8 until
-// the first pages are there (dependent loads) and 8 for the last join (65 KiB of
-// state a tile and range).  Eight prompts of 183-1659 tokens, d = 64, window 500:
-// 20 us (4 bits: 24).
+// Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096, 413 GFLOP: 392-445
+// us, card by card, 0.93-1.05 PFLOP/s, 0.73-0.80 of what a square product of 8192
+// reaches on the same card (1.28-1.39; over 4 bits 395-460, 8 bits 405-473).  Bound by
+// power: all 8192 keys for every query run at 1.79 GHz, not 2.4, with 55 % of the matrix
+// core's cycles taken, so shorter instruction sequences move nothing there (the weights
+// between the products of the scores, one after the other without a gap, took the same
+// time).  Direct loads and two scores in flight brought it from 502 us; deeper rings of
+// buffers, pages touched ahead in L2 (430 us), wave priorities and tiles of 64 rows
+// brought nothing; waves without queries that skip their products 2 % more on full tiles.
+// Eight chunks of 36 tokens behind a window of 4096, 64 heads over 8: 70-77 us (4 bits
+// 75-80, 8 bits 77-88).  Eight prompts of 183-1659 tokens, d = 64, window 500: 19-21 us.
+// 8 bits: 23523 tokens of eight prompts, f16, 610 GFLOP: 692-777 us, 0.63-0.67 of the
+// product's rate.  K and V of a page share one page's registers in turn: with both in hand
+// the kernel spilled (one prompt 498 us).  289 tokens behind 1024-32768 and a window of
+// 4096: 73-77 us.
+// CROSS: 2969 queries of eight rows of 1024-8192 states, 253 GFLOP: 288-320 us (with the
+// rows as they come 303-306 where sorted take 288-292).
 #pragma once
 
 #include <type_traits>

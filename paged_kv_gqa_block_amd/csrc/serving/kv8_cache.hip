@@ -11,7 +11,11 @@
 // subnormal codes).  A block that holds earlier tokens of its row keeps at least
 // its exponent, and those tokens are rounded again where it grows.
 //
-// Bound: bytes moved; there is no reuse.
+// Bound: bytes moved; there is no reuse.  Measured: 98000 tokens of 8 KV heads, d = 128,
+// f16: 129-137 us to quantise 401 MB into 201 (4.4-4.7 TB/s), 108-113 to read them back
+// (5.3-5.6; a large copy reaches 4.9); one token of 64 rows, most of them behind earlier ones of
+// their page: 4.4 and 3.5 us, a launch and a chain of four loads (offsets, page number,
+// scale and codes, and the store).
 //
 // One workgroup per (page of a row that the run touches, KV head): 16 tokens
 // by d channels.  Thread (token, chunk) holds eight channels of K and of V.
