@@ -39,11 +39,11 @@
 // brought nothing; waves without queries that skip their products 2 % more on full tiles.
 // Eight chunks of 36 tokens behind a window of 4096, 64 heads over 8: 70-77 us (4 bits
 // 75-80, 8 bits 77-88).  Eight prompts of 183-1659 tokens, d = 64, window 500: 19-21 us.
-// 8 bits: 23523 tokens of eight prompts, f16, 610 GFLOP: 692-777 us, 0.63-0.67 of the
+// 8 bits: 23523 tokens of eight prompts, f16, 610 GFLOP: 665-777 us, 0.63-0.70 of the
 // product's rate.  K and V of a page share one page's registers in turn: with both in hand
 // the kernel spilled (one prompt 498 us).  289 tokens behind 1024-32768 and a window of
-// 4096: 73-77 us.
-// CROSS: 2969 queries of eight rows of 1024-8192 states, 253 GFLOP: 288-320 us (with the
+// 4096: 70-77 us.
+// CROSS: 2969 queries of eight rows of 1024-8192 states, 253 GFLOP: 277-320 us (with the
 // rows as they come 303-306 where sorted take 288-292).
 #pragma once
 
