@@ -136,8 +136,9 @@ pkv_status pkv_cross_kv8(const pkv_problem* prob, const int32_t* tok_offsets, in
  * none), one row's behind the other's in the step's token-major arrays of
  * num_tokens rows.
  *   A row is served when its length and its new one lie in [0, max_pages_per_row *
- *   P], its tokens in the arrays, and the pages that it and the rows before it ask
- *   for in the free list; a row that needs no page is never short of them.  Served
+ *   P], its tokens in the arrays (a row without any is never outside them), and the
+ *   pages that it and the rows before it ask for in the free list; a row that needs
+ *   no page is never short of them.  Served
  *   rows take pages from the top of the stack, in row order, into their tables, and
  *   grow by their counts; the others stay as they are.
  *   Written for the step's calls:

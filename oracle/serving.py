@@ -150,7 +150,7 @@ class Pages:
             first, total = total, total + c
             off.append(min(total, num_tokens))
             n = self.lens[r]
-            ok = 0 <= n <= cap and n + c <= cap and total <= num_tokens
+            ok = 0 <= n <= cap and n + c <= cap and (c == 0 or total <= num_tokens)
             need = -(-(n + c) // 16) + -n // 16 if ok else 0
             asked += need
             ok = ok and (need == 0 or asked <= have)

@@ -117,7 +117,9 @@ __global__ __launch_bounds__(kThreads) void take_kernel(TakeArgs a) {
     for (int i = 0; i < kRowsPerThread; ++i) {
       s_off[int(threadIdx.x) * kRowsPerThread + i] = before;
       upto[i] = before = min(before + min(static_cast<uint32_t>(cnt[i]), most), most);
-      ok[i] = len[i] >= 0 && len[i] <= cap && cnt[i] <= cap - len[i] && upto[i] < most;
+      // (A row without tokens has none outside the arrays, whatever the rows before it bring.)
+      ok[i] = len[i] >= 0 && len[i] <= cap && cnt[i] <= cap - len[i] &&
+              (cnt[i] == 0 || upto[i] < most);
       need[i] = ok[i] ? pages_of(len[i] + cnt[i]) - pages_of(len[i]) : 0;
       wants += static_cast<uint32_t>(need[i]);
     }

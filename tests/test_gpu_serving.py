@@ -790,6 +790,24 @@ def test_tables_that_do_not_hold_together():
         assert t.state[0].item() == (0 if count < 0 else pool - 1)
 
 
+@pytest.mark.parametrize("rows,num_tokens", [(2, 8), (70, 600), (1100, 40), (1100, 600)])
+def test_rows_without_tokens_behind_those_that_overflow(rows, num_tokens):
+    """They keep their length: one workgroup and several, rows of a later scan too."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(1, 40, rows).tolist()
+    held = sum(-(-n // 16) for n in lens)
+    t, ref = _table(lens, 40, held + 40, 60, num_tokens, rng)
+    counts = np.zeros(rows, dtype=np.int64)
+    counts[0], counts[rows // 2] = num_tokens // 2 + 1, num_tokens // 2
+    say(f"[pages] {rows} rows, {num_tokens} tokens and one more")
+    got = t.take(_i32(counts))
+    torch.cuda.synchronize()
+    _check_take(t, ref, counts, num_tokens, got)
+    assert got["seq_lens"].tolist()[-1] == (lens[-1] if rows > 2 else 0)
+    assert got["seq_lens"].tolist()[1:rows // 2] == lens[1:rows // 2]
+    assert t.state[1].item() == 1
+
+
 def test_new_table_and_no_tokens():
     prob = engine.make_problem(2, 1, 1, 64, 16, 5, 4, "f16")
     t = engine.PageTable(prob, 40)

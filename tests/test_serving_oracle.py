@@ -130,3 +130,14 @@ def test_a_row_short_of_pages_holds_up_those_behind_it():
     p = sv.Pages([16] * 4, [[0, -1, -1], [1, -1, -1], [2, -1, -1], [3, -1, -1]], [9], 10, 3)
     seq, off, slots, positions, denied = p.take([17, 1, 0, 1], 50)
     assert seq == [0, 0, 16, 0] and denied == 3 and p.free == [9]
+
+
+def test_rows_without_tokens_stay_as_long_as_they_are():
+    """Behind a row whose tokens pass the arrays, before it, and under a table that is
+    full: nothing of theirs lies outside."""
+    p = sv.Pages([20, 33, 0, 64, 16], [[0, 1, -1, -1], [2, 3, 4, -1], [-1] * 4, [5, 6, 7, 8],
+                                       [9, -1, -1, -1]], [10, 11], 12, 4)
+    seq, off, slots, positions, denied = p.take([0, 9, 0, -3, 2], 8)
+    assert seq == [20, 0, 0, 64, 0] and off == [0, 0, 8, 8, 8, 8] and denied == 2
+    assert p.lens == [20, 33, 0, 64, 16] and p.free == [10, 11]
+    assert set(slots.values()) == set(positions.values()) == {-1}
