@@ -163,7 +163,8 @@ pkv_status pkv_pages_take(const pkv_problem* prob, const int32_t* counts, int32_
  * back on the stack, the last row's last page first, and their table entries
  * become -1.  A row that is no longer than that, or whose keep is negative, is left
  * alone.  After a pkv_pages_take, giving back what it took restores the stack.
- * Pages that the stack has no room for are dropped (it has, unless a page was in two
+ * Entries outside [0, num_pool_pages) do not go on the stack.  Pages that it has no
+ * room for, these entries counted, are dropped (it has, unless a page was in two
  * tables).  Errors as above.
  */
 pkv_status pkv_pages_release(const pkv_problem* prob, const int32_t* keep, int32_t* lens,

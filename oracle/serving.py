@@ -168,12 +168,14 @@ class Pages:
         return seq, off, slots, positions, denied
 
     def release(self, keep):
+        room = self.pool - len(self.free)  # taken by numbers outside the pool too
         for r in reversed(range(len(self.lens))):
             n, k = self.lens[r], int(keep[r])
             if not 0 <= n <= self.width * 16 or k < 0 or k >= n:
                 continue
             for e in reversed(range(-(-k // 16), -(-n // 16))):
-                if len(self.free) < self.pool:
+                if room > 0 and 0 <= self.table[r][e] < self.pool:
                     self.free.append(self.table[r][e])
                 self.table[r][e] = -1
+                room -= 1
             self.lens[r] = k

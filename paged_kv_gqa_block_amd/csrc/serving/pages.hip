@@ -6,7 +6,9 @@
 // row i is served where its tokens fit the call's arrays and the table and the sum of
 // need_k, k <= i, fits the free list; its page of rank m among all that are asked for
 // is free[count - 1 - m].  Released pages go on top, the last row's last page first, so
-// that giving back what a call took restores the list.
+// that giving back what a call took restores the list.  Entries of a table that name no
+// page of the pool go there too and come out again: where a workgroup met one, the last to
+// finish closes the list's gaps.
 //
 // Bound: latency.  A step of 64 rows reads and writes a few KB behind a chain of three
 // dependent loads (lengths, free list, table); 256 rows of 130000 tokens write
@@ -211,13 +213,38 @@ __global__ __launch_bounds__(kThreads) void take_kernel(TakeArgs a) {
   }
 }
 
+// Past the L2, for the workgroup that closes gaps (7600 pages of many workgroups: 0.4 us more
+// than into the L2).
+__device__ __forceinline__ void put_page(int32_t* p, int page) {
+  __hip_atomic_store(p, page, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// As last_to_arrive; in the last workgroup `any` becomes true where it was in one of them
+// (the counter's upper half counts those).
+__device__ __forceinline__ bool last_of_any(int32_t* counter, int ns, bool& any, int* s_last) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int was = __hip_atomic_fetch_add(counter, any ? 0x10001 : 1, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = (was & 0xffff) == ns - 1;
+    if (last) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *s_last = !last ? 0 : any || was > 0xffff ? 2 : 1;
+  }
+  __syncthreads();
+  any = *s_last == 2;
+  return *s_last != 0;
+}
+
 __global__ __launch_bounds__(kThreads) void release_kernel(ReleaseArgs a) {
   __shared__ uint32_t s_upto[kChunk];  // pages up to and with a row, from the last row on
   __shared__ int s_end[kChunk];        // block-table entry behind its last page
   __shared__ uint32_t s_wave[4];
-  __shared__ bool s_last;
+  __shared__ bool s_gap;               // an entry released here names no page of the pool
+  __shared__ int s_last;
   const int cap = a.max_pages * 16;
   const int free = free_count(a.state, a.num_pool_pages);
+  if (threadIdx.x == 0) s_gap = false;
   // The new length of a row: `keep` where that is shorter.
   auto kept = [&](int r, int& len) {
     len = a.lens[r];
@@ -272,21 +299,40 @@ __global__ __launch_bounds__(kThreads) void release_kernel(ReleaseArgs a) {
       const int entry = s_end[at] - 1 - static_cast<int>(next - before);
       int32_t* from = a.block_table + int64_t(a.batch - 1 - r0 - at) * a.max_pages + entry;
       const int64_t to = int64_t(free) + next;
-      if (to < a.num_pool_pages) a.free_pages[to] = *from;
+      const int page = *from;
+      if (to < a.num_pool_pages) {
+        put_page(a.free_pages + to, page);
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pool_pages)) s_gap = true;
+      }
       *from = -1;
     }
     __syncthreads();
   }
-  if (!alone && !last_to_arrive(a.state + kStateArrivals, gridDim.x, &s_last)) return;
-  __syncthreads();
+  bool gap = s_gap;
+  if (!alone && !last_of_any(a.state + kStateArrivals, gridDim.x, gap, &s_last)) return;
+  uint32_t listed = min(total, static_cast<uint32_t>(a.num_pool_pages - free));
+  if (gap) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this workgroup's pages are in the list
+    __syncthreads();
+    const uint32_t upto = listed;
+    listed = 0;
+    for (uint32_t i0 = 0; i0 < upto; i0 += kThreads) {
+      const uint32_t i = i0 + threadIdx.x;
+      const int page = i < upto ? __hip_atomic_load(a.free_pages + free + i, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT)
+                                : -1;
+      const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pool_pages);
+      // No page moves up, and all of these are read before the first is written.
+      const uint32_t to = scan_before(in ? 1 : 0, listed, 0x7fffffffu, s_wave);
+      if (in) put_page(a.free_pages + free + to, page);
+    }
+  }
   for (int r = threadIdx.x; r < a.batch; r += kThreads) {
     int len;
     const int keep = kept(r, len);
     if (keep != len) a.lens[r] = keep;
   }
-  if (threadIdx.x == 0)
-    a.state[kStateFree] =
-        static_cast<int>(min(int64_t(free) + total, int64_t(a.num_pool_pages)));
+  if (threadIdx.x == 0) a.state[kStateFree] = free + static_cast<int>(listed);
 }
 
 }  // namespace

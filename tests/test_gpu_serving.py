@@ -808,6 +808,35 @@ def test_rows_without_tokens_behind_those_that_overflow(rows, num_tokens):
     assert t.state[1].item() == 1
 
 
+@pytest.mark.parametrize("rows,longest,every", [(1, 60, 2), (5, 900, 7), (60, 3000, 50),
+                                                (60, 3000, 1), (1500, 100, 30)])
+def test_entries_that_name_no_page_do_not_come_back(rows, longest, every):
+    """Released by one workgroup and by several: the list holds pages alone, in their
+    order, and rows that take them are whole."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(1, longest + 1, rows).tolist()
+    held = sum(-(-n // 16) for n in lens)
+    t, ref = _table(lens, 9, held + 9, 400, 5000, rng)
+    table = np.array(ref.table)
+    bad = (rng.integers(0, every, table.shape) == 0) & (table >= 0)
+    table[bad] = rng.choice([-1, held + 9, 2 ** 31 - 1, -2 ** 31], int(bad.sum()))
+    ref.table = table.tolist()
+    t.block_table.copy_(_i32(table))
+    say(f"[pages] {int(bad.sum())} of {held} entries name no page")
+    for keep in (rng.integers(0, longest, rows), np.zeros(rows, dtype=np.int64)):
+        t.release(_i32(keep))
+        torch.cuda.synchronize()
+        ref.release(keep)
+        _check_table(t, ref)
+    assert not bad.any() or len(ref.free) < held + 9
+    counts = rng.integers(0, 2 * 5000 // rows + 1, rows)
+    got = t.take(_i32(counts))
+    torch.cuda.synchronize()
+    n = _check_take(t, ref, counts, 5000, got)
+    served = torch.repeat_interleave(got["seq_lens"] > 0, got["tok_offsets"].diff())
+    assert (got["slots"][:n][served] >= 0).all()
+
+
 def test_new_table_and_no_tokens():
     prob = engine.make_problem(2, 1, 1, 64, 16, 5, 4, "f16")
     t = engine.PageTable(prob, 40)

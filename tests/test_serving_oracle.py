@@ -141,3 +141,15 @@ def test_rows_without_tokens_stay_as_long_as_they_are():
     assert seq == [20, 0, 0, 64, 0] and off == [0, 0, 8, 8, 8, 8] and denied == 2
     assert p.lens == [20, 33, 0, 64, 16] and p.free == [10, 11]
     assert set(slots.values()) == set(positions.values()) == {-1}
+
+
+def test_entries_that_name_no_page_do_not_come_back():
+    p = sv.Pages([64, 20], [[5, -1, 9, 7], [6, 2, -1, -1]], [1, 0], 8, 4)
+    p.release([10, 0])
+    assert p.free == [1, 0, 2, 6, 7] and p.table == [[5, -1, -1, -1], [-1] * 4]
+    seq, _, slots, _, denied = p.take([0, 64], 64)
+    assert denied == 0 and seq == [10, 64] and min(slots.values()) >= 0
+    # Room for three: the last row's two, then one that is none.
+    p = sv.Pages([48, 32], [[0, 1, 8, -1], [2, 3, -1, -1]], [4, 5, 6, 7, 4], 8, 4)
+    p.release([0, 0])
+    assert p.free == [4, 5, 6, 7, 4, 3, 2]
