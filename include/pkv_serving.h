@@ -108,8 +108,13 @@ int32_t pkv_prompt_kv8_splits(const pkv_problem* prob, const pkv_view* view, int
  *     units (0 on an invalid argument).
  *   workspace: pkv_cross_workspace_bytes device bytes (0 for one split and where
  *     the call would be refused), on the terms of pkv_attend_window's; one_per_row
- *     says that the call passes no tok_offsets.
- * Errors: as pkv_prompt_window's; PKV_ERANGE also where tiles of sixteen queries,
+ *     says that the call passes no tok_offsets.  The size falls where calls become ones
+ *     of many queries.  A call of few queries takes no more ranges than its workspace
+ *     holds, so that of a larger step of the same problem, in two splits or more, does
+ *     for it too; with all of its ranges only if it has its own size, the largest over
+ *     the steps.
+ * Errors: as pkv_prompt_window's, PKV_ENOSPC of few queries where the workspace does
+ * not hold two ranges; PKV_ERANGE also where tiles of sixteen queries,
  * (num_tokens * G / 16 + B) * Hkv, times max_splits pass 2^24 - 1, or 65536 in splits.
  */
 size_t pkv_cross_workspace_bytes(const pkv_problem* prob, int32_t num_tokens, int32_t one_per_row,

@@ -158,6 +158,20 @@ Workspace cross_workspace_of(const pkv_problem* p, int64_t tiles, int32_t splits
   return w;
 }
 
+// The ranges, up to max_splits, whose states a workspace holds; 1: not even two.  A
+// workspace for two ranges or more of a call of many queries holds two of any call of
+// few over the same problem, so it is never too small for a smaller step: up to 64 (32)
+// queries a row make 5 (3) tiles of 16 states a row and range, more of them 1.5 (1.25) and
+// more tiles of 128 a row.
+int32_t cross_splits_in(const pkv_problem* p, int64_t tiles, int32_t max_splits, size_t bytes) {
+  const size_t one = static_cast<size_t>(tiles) * p->num_kv_heads * kCrossRows *
+                     (p->head_dim + 2) * sizeof(float);
+  if (bytes < kCounterBytes) return 1;
+  size_t s = std::min<size_t>((bytes - kCounterBytes) / one, max_splits);
+  while (s > 1 && cross_workspace_of(p, tiles, static_cast<int32_t>(s)).bytes > bytes) --s;
+  return static_cast<int32_t>(std::max<size_t>(s, 1));
+}
+
 pkv_status cross(const pkv_problem* prob, const int32_t* tok_offsets, int32_t num_tokens,
                  const int32_t* seq_lens, int32_t max_splits, const void* q, Pools pools,
                  const int32_t* block_table, void* workspace, size_t workspace_bytes, void* out,
@@ -181,8 +195,9 @@ pkv_status cross(const pkv_problem* prob, const int32_t* tok_offsets, int32_t nu
   if (!cross_fits(prob, tiles, max_splits)) return PKV_ERANGE;
   AttendArgs a{};
   if (max_splits > 1) {
+    max_splits = cross_splits_in(prob, tiles, max_splits, workspace_bytes);
+    if (max_splits < 2) return PKV_ENOSPC;
     const Workspace w = cross_workspace_of(prob, tiles, max_splits);
-    if (workspace_bytes < w.bytes) return PKV_ENOSPC;
     char* ws = static_cast<char*>(workspace);
     a.arrivals = reinterpret_cast<int32_t*>(ws);
     a.st_ml = reinterpret_cast<float*>(ws + w.ml);

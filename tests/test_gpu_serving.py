@@ -672,6 +672,27 @@ def test_workspace_of_all_shapes():
     assert not ws[:256 << 10].any()
 
 
+@pytest.mark.parametrize("kind", [16, 4, 8])
+def test_cross_in_a_workspace_of_fewer_ranges(kind):
+    """As many ranges as the workspace holds, and nothing behind it is written."""
+    b = make_cross(kind, 7, [3000, 1200, 40], [3, 2, 6], hkv=2, group=4)
+    prob, w = b.problem(), b.device()
+    step, ref = engine.CrossStep(prob, 11, 40), cross_reference(b)
+    for room in (2, 3, 7, 39):
+        n = _serving.pkv_cross_workspace_bytes(prob, 11, False, room) + 15
+        ws = torch.zeros(n + (1 << 20), dtype=torch.uint8, device="cuda")
+        ws[n:] = 77
+        step._own = (ws.data_ptr(), n, *step._own[2:])
+        for i in range(2):
+            say(f"[room for {room} ranges] {i}")
+            step.out.fill_(float("nan"))
+            out, lse = step.run(w)
+            torch.cuda.synchronize()
+            check(out, lse, ref, "f16", 128, b.vmax, False, f"{room} ranges")
+        assert (ws[n:] == 77).all() and not ws[:256 << 10].any()
+        assert ws[256 << 10:n - 15].any()
+
+
 # ---- page tables -------------------------------------------------------------------------
 
 def _table(lens, free, pool, width, num_tokens, rng):

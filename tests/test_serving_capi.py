@@ -209,6 +209,37 @@ def test_cross_sizes_over_the_whole_range():
     assert ws(p, 4, False, 3) >= (256 << 10) + (4 * 4 // 16 + 2) * 2 * 3 * 16 * (128 + 2) * 4
 
 
+# PKV_EHIP: every check is passed and there is no GPU to launch on.  (With one, nothing
+# may be launched over these addresses: sizes alone are compared there.)
+GPU = os.path.exists("/dev/kfd")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_workspace_does_for_every_smaller_step(kind):
+    """Calls of any number of queries over the workspace of the largest, around the border
+    between few and many, at fixed splits and at each step's own."""
+    ws, sp = _serving.pkv_cross_workspace_bytes, _serving.pkv_cross_splits
+    fell = 0
+    for b, hq, hkv, d in ((8, 32, 8, 128), (1, 16, 1, 64), (5, 15, 5, 128), (40, 64, 8, 64)):
+        p = _prob(batch=b, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, max_pages_per_row=2048)
+        few = (64 if b * hkv <= 64 else 32) * b * hkv // hq  # the last call of few queries
+        for splits in (2, 3, 17, 64):
+            for most in (few - 1, few, few + 1, 2 * few, 40 * few):
+                room = ws(p, most, False, splits)
+                for n in {1, 2, b, few // 2, few - 1, few, few + 1, most}:
+                    if n > most:
+                        continue
+                    fell += ws(p, n, False, splits) > room
+                    for s in {2, splits, max(sp(p, n, False, 256), 2)} if n <= few else {splits}:
+                        if not GPU:
+                            got = _cross(kind, p, n=n, splits=s, ws=P, ws_bytes=room)
+                            assert got == _lib.PKV_EHIP, (b, hq, n, s, most, splits)
+                            got = _cross(kind, p, n=n, splits=s, ws=P,
+                                         ws_bytes=min(ws(p, n, False, 2), room) - 1)
+                            assert got == PKV_ENOSPC or n > few, (b, hq, n, s, most, splits)
+    assert fell  # sizes that are not the largest step's
+
+
 def test_pages_refusals():
     def take(prob=None, counts=P, n=10, lens=P, bt=P, free=P, state=P, seq=P, off=P):
         return _lib.LIB.pkv_pages_take(ctypes.byref(prob or _prob()), counts, n, lens, bt, free,
