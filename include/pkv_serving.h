@@ -17,8 +17,10 @@
  * rounded again.  An element becomes x / 2^e rounded to the nearest code, ties to
  * even, saturating at 448; an infinity or a NaN becomes NaN, and reads back as
  * NaN.  The value that a code stands for is exact in the problem's type.  It is
- * off by at most 2^-4 of the element, or 2^(e - 10) where that is more, unless its
- * magnitude passes 448 * 2^7 (448 * 2^119).  Byte order of a page:
+ * off by at most 2^-4 of the element, or 2^(e - 10) where that is more; where the
+ * block has grown since, these roundings add up, and it is off by less than 2^(e - 9)
+ * where that is more than 2^-4 of the element.  (Elements whose magnitude passes 448 *
+ * 2^7, PKV_BF16 448 * 2^119, saturate instead.)  Byte order of a page:
  * csrc/serving/kv8_common.h.  One pool serves one dtype.
  *
  * Cross attention.  Every query of row i sees all N_i = seq_lens[i] tokens of

@@ -5,11 +5,14 @@
 // e = floor(log2 max|x|) - 8 (+ 1 where max|x| > 448 * 2^e), the smallest that holds
 // every finite element of the run's tokens in the block; its codes are x / 2^e rounded
 // to e4m3, ties to even.  e4m3 is off by at most 2^-4 of an element (half a step of
-// three bits of mantissa) as long as that is 2^-14 of the block's largest or more, so a
-// scale between two powers of two would gain nothing; whole powers keep every value
-// exact in 16 bits, and rescaling exact but for what falls below 2^-6 (a block's
-// subnormal codes).  A block that holds earlier tokens of its row keeps at least
-// its exponent, and those tokens are rounded again where it grows.
+// three bits of mantissa) as long as that is 2^(e - 6) or more, so always at 2^-13 of the
+// block's largest (2^(e - 6) over more than 224 * 2^e).  A scale between two powers of
+// two would gain nothing; whole powers keep every value exact in 16 bits, and rescaling
+// exact but for what falls below 2^(e - 6) (a block's subnormal codes).  A block that
+// holds earlier tokens of its row keeps at least its exponent, and those tokens are
+// rounded again where it grows: by 2^(e - 10) at most each time.  The rounding before the
+// first of these was of at most 2^(e - 11) (what falls below 2^(e - 6) had steps of
+// 2^(e - 10)), or one of a subnormal code too, so that all make less than 2^(e - 9).
 //
 // Bound: bytes moved; there is no reuse.  Measured: 98000 tokens of 8 KV heads, d = 128,
 // f16: 129-137 us to quantise 401 MB into 201 (4.4-4.7 TB/s), 108-113 to read them back

@@ -153,3 +153,50 @@ def test_entries_that_name_no_page_do_not_come_back():
     p = sv.Pages([48, 32], [[0, 1, 8, -1], [2, 3, -1, -1]], [4, 5, 6, 7, 4], 8, 4)
     p.release([0, 0])
     assert p.free == [4, 5, 6, 7, 4, 3, 2]
+
+
+def test_errors_of_growing_blocks():
+    """Off by at most 2^-4 of the element, or less than 2^(e - 9), at the block's last
+    exponent, however often it has grown; 2^(e - 10) and no more where it has not."""
+    def run(steps, dtype):
+        """Values and elements of a block whose tokens come one after the other."""
+        c = sv.Cache8(1, 1, 64, dtype)
+        x = np.zeros((len(steps), 2, 1, 64))
+        for t, z in enumerate(steps):
+            x[t] = z
+            c.store(0, t, x[t:t + 1])
+        return np.stack([c.values(0, t) for t in range(len(steps))]), x, c.scales
+
+    # 2.5 steps of a subnormal code: 2, then nothing; more than 2^(e - 10) in all.
+    small = np.zeros(64)
+    small[:2] = 448.0, 2.5 * 2.0 ** -9
+    y, x, scales = run([small, 1792.0], "f16")
+    assert scales[0, 0, 0] == 127 + 2 and y[0, 0, 0, 1] == 0.0
+    assert 2.0 ** (2 - 10) < abs(y[0, 0, 0, 1] - x[0, 0, 0, 1]) < 2.0 ** (2 - 9)
+
+    rng = np.random.default_rng(6)
+    past = 0
+    for trial in range(300):
+        dtype, t = (("f16", torch.float16), ("bf16", torch.bfloat16))[trial % 2]
+        tops = 2.0 ** np.sort(rng.integers(-12, 14, 16))
+        z = rng.uniform(0.5, 1, (16, 64)) * tops[:, None] * 2.0 ** rng.integers(-18, 1, (16, 64))
+        z[:, 0] = tops
+        z = torch.from_numpy(z * rng.choice([-1, 1], z.shape)).to(t).double().numpy()
+        y, x, scales = run(z[:, None, None], dtype)
+        e = scales[0].astype(int).T[..., None] - 127
+        off, rel = np.abs(y - x), 2.0 ** -4 * np.abs(x)
+        assert ((off <= rel) | (off < 2.0 ** (e - 9.0))).all()
+        last = off[-1]  # never rounded again
+        assert (last <= np.maximum(rel[-1], 2.0 ** (e - 10.0))).all()
+        past += int((off > np.maximum(rel, 2.0 ** (e - 10.0))).sum())
+    assert past  # the bound of one rounding does not hold for all
+
+    # Where 2^-4 of the element no longer holds: below 2^(e - 6), 2^-13 of any largest.
+    for top in (240.0, 448.0):
+        z = np.full(64, 7.5 * 2.0 ** -9)
+        z[0] = top
+        y, x, _ = run([z], "f16")
+        assert abs(y - x).max() == 2.0 ** -10 > 2.0 ** -4 * 7.5 * 2.0 ** -9
+    z = np.concatenate([[225.0], 225.0 * 2.0 ** -13 * np.linspace(1, 2, 63)])
+    y, x, scales = run([z], "bf16")
+    assert scales[0, 0, 0] == 127 and (np.abs(y - x) <= 2.0 ** -4 * np.abs(x)).all()
