@@ -512,6 +512,11 @@ class PromptStep(_ContextCalls):
     ``run`` takes q [num_tokens][Hq][d], tok_offsets [B + 1] (or None for one
     token per row), block_table, seq_lens and k_pool, v_pool or kv4_pool or
     kv8_pool, kv8_scales.
+
+    `splits`: over 16 and 4 bits the ranges that a tile cuts its keys into at most, over
+    8 bits the workgroups of a KV head that its tiles are spread over (pkv_prompt_kv8);
+    None: as many as fill the device.  The first call over 8 bits may allocate a
+    workspace: make one before a capture, or the graph clears its own at every call.
     """
 
     def __init__(self, prob: _lib.pkv_problem, num_tokens: int, window: int = 0, sinks: int = 0,
@@ -524,12 +529,13 @@ class PromptStep(_ContextCalls):
             cus = torch.cuda.get_device_properties(self.device).multi_processor_count
             self.splits = _context.pkv_prompt_splits(prob, self.view, num_tokens, False, cus)
             self.splits8 = _serving.pkv_prompt_kv8_splits(prob, self.view, num_tokens, False, cus)
-        # Room for calls over every kind of cache, and without tok_offsets too.
+        # Room for calls without tok_offsets too.
         ways = (False, True) if num_tokens == prob.batch else (False,)
-        nbytes = max(max(_context.pkv_prompt_workspace_bytes(prob, num_tokens, one, self.splits),
-                         _serving.pkv_prompt_kv8_workspace_bytes(prob, num_tokens, one,
-                                                                 self.splits8))
+        nbytes = max(_context.pkv_prompt_workspace_bytes(prob, num_tokens, one, self.splits)
                      for one in ways)
+        self._bytes8 = max(_serving.pkv_prompt_kv8_workspace_bytes(prob, num_tokens, one,
+                                                                   self.splits8) for one in ways)
+        self._workspace8 = self._captured8 = None
         self.workspace = _workspace(nbytes, self.device)
         self.out = torch.empty(num_tokens, prob.num_q_heads, prob.head_dim, dtype=self.dtype,
                                device=self.device)
@@ -544,9 +550,36 @@ class PromptStep(_ContextCalls):
         q = self._expect("q", w["q"], self.out.shape, self.dtype)
         table, lens = self._tables(w["block_table"], w["seq_lens"])
         pools, kind = self._pools(w), self._kind(w)
-        return ("pkv_prompt_" + kind, self._view_ref, self._offsets(w.get("tok_offsets"), n), n,
-                lens, self.splits8 if kind == "kv8" else self.splits, q, *pools, table,
-                *self._own, self._stream(stream))
+        off = self._offsets(w.get("tok_offsets"), n)
+        splits, own = ((self.splits8, self._own8(stream)) if kind == "kv8" else
+                       (self.splits, self._own))
+        return ("pkv_prompt_" + kind, self._view_ref, off, n, lens, splits, q, *pools, table,
+                *own, self._stream(stream))
+
+    def _own8(self, stream) -> tuple:
+        """``_own`` of a call over 8 bits.  Where its workspace is the larger one, it is made
+        at the first such call, so that steps over the other caches do without.  One made in
+        a capture is cleared by the graph, before each call: eager calls get their own."""
+        if self._bytes8 <= self._own[1]:
+            return self._own
+        ws = self._workspace8
+        if ws is None:
+            at = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            with torch.cuda.device(self.device), torch.cuda.stream(at):
+                if torch.cuda.is_current_stream_capturing():
+                    if self._captured8 is None:
+                        self._captured8 = torch.empty(self._bytes8, dtype=torch.uint8,
+                                                      device=self.device)
+                        self._buffers += (self._captured8,)
+                    ws = self._captured8
+                    ws[:256 << 10].zero_()
+                else:
+                    if self._ready is not None:  # behind the fills of the other buffers
+                        torch.cuda.current_stream().wait_event(self._ready)
+                    ws = self._workspace8 = _workspace(self._bytes8, self.device)
+                    self._own_buffers(*self._buffers, ws)
+            self._known.clear()  # so that every stream is recorded on the new buffer
+        return (ws.data_ptr(), self._bytes8, *self._own[2:])
 
     def run(self, w: dict, stream=None) -> tuple:
         return self.run_bound(self.bind(w, stream))

@@ -693,6 +693,91 @@ def test_cross_in_a_workspace_of_fewer_ranges(kind):
         assert ws[256 << 10:n - 15].any()
 
 
+def _shares_step():
+    """A prompt whose 8-bit shares take more workspace than its ranges."""
+    b = Batch8(71, [3000, 2500], [40, 24], hkv=4, group=4)
+    prob = b.problem()
+    step = engine.PromptStep(prob, 64)
+    step.splits, step.splits8 = 1, 12  # as a larger problem's caps would have it
+    step.workspace = torch.empty(0, dtype=torch.uint8, device="cuda")
+    step._own = (0, 0, *step._own[2:])
+    step._bytes8 = _serving.pkv_prompt_kv8_workspace_bytes(prob, 64, False, 12)
+    assert step._bytes8 > 0
+    return b, step
+
+
+def test_prompts_over_other_caches_pay_for_no_shares():
+    """A step's workspace is that of its ranges; 8 bits get theirs at their first call."""
+    from paged_kv_gqa_block_amd import _context
+    for heads, new, rows in ((32, 1024, 8), (32, 1900, 1), (64, 289, 8)):
+        prob = engine.make_problem(rows, heads, 8, 128, 16, 64, 512, "bf16")
+        cus = torch.cuda.get_device_properties(0).multi_processor_count
+        step = engine.PromptStep(prob, new)
+        n = _context.pkv_prompt_splits(prob, step.view, new, False, cus)
+        assert step.workspace.numel() == _context.pkv_prompt_workspace_bytes(prob, new, False, n)
+    b, step = _shares_step()
+    w, ref = b.device(), b.reference()
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    for i, stream in enumerate((None, torch.cuda.Stream(), torch.cuda.Stream())):
+        say(f"[workspace of shares] {i}")
+        out, lse = step.run(w, stream)
+        torch.cuda.synchronize()
+        check(out, lse, ref, "f16", 128, b.vmax, True, "shares")
+        if i == 0:
+            grown = torch.cuda.memory_allocated() - held
+            assert step._bytes8 <= grown < step._bytes8 + (4 << 20)
+    assert torch.cuda.memory_allocated() - held <= grown
+    assert not step._workspace8[:256 << 10].any()
+
+
+def test_workspace_of_shares_first_needed_on_a_busy_stream():
+    """Its counters are zero before the call, on whatever stream the step was built."""
+    building, running = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(building):
+        b, step = _shares_step()
+        w = b.device()
+    torch.cuda.synchronize()
+    say("[workspace of shares] busy streams")
+    with torch.cuda.stream(building):
+        junk = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+        del junk
+        _busy(building)
+        step.run(w, running)  # the workspace is made here
+        running.synchronize()
+        out, lse = step.run(w)
+    torch.cuda.synchronize()
+    check(out, lse, b.reference(), "f16", 128, b.vmax, True, "shares")
+    assert not step._workspace8[:256 << 10].any()
+
+
+def test_workspace_of_shares_first_needed_in_a_capture():
+    """The graph clears the workspace it was captured with; eager calls before and between
+    its replays have their own."""
+    b, step = _shares_step()
+    w, ref = b.device(), b.reference()
+    q = w["q"].clone()
+    graph, again = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step.run(w)
+        out, lse = step.run(w)
+    with torch.cuda.graph(again):
+        step.run(w)
+    assert step._workspace8 is None
+    for i in range(4):
+        for what in (graph.replay, lambda: step.run(w), again.replay, lambda: step.run(w)):
+            say(f"[workspace of shares] replay {i}")
+            out.fill_(float("nan"))
+            w["q"].copy_(q if i % 2 == 0 else -q)
+            what()
+            torch.cuda.synchronize()
+            if i % 2 == 0:
+                check(out, lse, ref, "f16", 128, b.vmax, True, "shares")
+            assert torch.isfinite(out).all()
+    assert step._workspace8.data_ptr() != step._captured8.data_ptr()
+
+
 # ---- page tables -------------------------------------------------------------------------
 
 def _table(lens, free, pool, width, num_tokens, rng):
