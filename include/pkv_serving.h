@@ -102,7 +102,7 @@ int32_t pkv_prompt_kv8_splits(const pkv_problem* prob, const pkv_view* view, int
  * (NULL: one per row, num_tokens = B), over 16-bit pages, the 4-bit or the 8-bit
  * pool.  q, out [num_tokens][Hq][d], lse [num_tokens][Hq] (may be NULL).  A query
  * of a row without tokens gets out = 0, lse = -inf.
- *   Calls of few queries a row (by num_tokens, B and G alone) keep 16 or more bits of
+ *   Calls of few queries a row (by num_tokens, B, Hq and Hkv alone) keep 16 or more bits of
  *   a weight in the second product, as decode does; calls of many round it to the
  *   problem's type, as prompts do.  Statistics and sums are held in fp32.
  *   max_splits: few queries: a tile cuts its keys into up to this many ranges; many:

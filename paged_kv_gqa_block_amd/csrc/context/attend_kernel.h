@@ -35,7 +35,8 @@
 // pages, three on their way, spill (393 us).
 // CROSS: four queries of 16 rows of 200-1500 states, 16 heads, d = 64, 16 bits (56 MB): 16 us;
 // 1-4 of 64 rows of 500-8000, G = 4, 8 bits (579 MB): 112-114 us, 5.1 TB/s; one to four of
-// 16 rows of 3000-4000, 16 bits (229 MB): 40-43 us.
+// 16 rows of 3000-4000, 16 bits (229 MB): 40-43 us.  4 bits: 1-4 of 64 rows of 500-8000,
+// G = 4 (310 MB) 72 us, 4.3 TB/s; four of 16 rows of 200-1500, 16 heads, d = 64 (15 MB) 12.
 //
 // Measured (G = 8, d = 128, 64 rows, 8 KV heads, bf16): 4 bits, 1.1 million
 // tokens (1.21 GB): 212-227 us, 5.3-5.7 TB/s; the same pages read and not used take

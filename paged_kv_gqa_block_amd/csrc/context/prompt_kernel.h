@@ -31,8 +31,9 @@
 // Measured (bf16, d = 128): 8192 tokens, 32 heads over 8, window 4096, 413 GFLOP: 392-445
 // us, card by card, 0.93-1.05 PFLOP/s, 0.73-0.80 of what a square product of 8192
 // reaches on the same card (1.28-1.39; over 4 bits 395-460, 8 bits 405-473).  Bound by
-// power: all 8192 keys for every query run at 1.79 GHz, not 2.4, with 55 % of the matrix
-// core's cycles taken, so shorter instruction sequences move nothing there (the weights
+// power: it runs at 1.96 GHz, not 2.4, and all 8192 keys for every query at 1.89, with 52
+// and 55 % of the matrix core's cycles taken and 50 of the vector unit's (the product at
+// 1.91 GHz, 70 and 28 %), so shorter instruction sequences move nothing there (the weights
 // between the products of the scores, one after the other without a gap, took the same
 // time).  Direct loads and two scores in flight brought it from 502 us; deeper rings of
 // buffers, pages touched ahead in L2 (430 us), wave priorities and tiles of 64 rows
@@ -40,11 +41,13 @@
 // Eight chunks of 36 tokens behind a window of 4096, 64 heads over 8: 70-77 us (4 bits
 // 75-80, 8 bits 77-88).  Eight prompts of 183-1659 tokens, d = 64, window 500: 19-21 us.
 // 8 bits: 23523 tokens of eight prompts, f16, 610 GFLOP: 665-777 us, 0.63-0.70 of the
-// product's rate.  K and V of a page share one page's registers in turn: with both in hand
+// product's rate, at 2.09 GHz with 43 % of the matrix core's cycles and 52 of the vector
+// unit's, which converts as well.  K and V of a page share one page's registers in turn: with both in hand
 // the kernel spilled (one prompt 498 us).  289 tokens behind 1024-32768 and a window of
-// 4096: 70-77 us.
+// 4096: 70-77 us, bound by latency (2.39 GHz, 25 and 34 %).
 // CROSS: 2969 queries of eight rows of 1024-8192 states, 253 GFLOP: 277-320 us (with the
-// rows as they come 303-306 where sorted take 288-292).
+// rows as they come 303-306 where sorted take 288-292), 2.09 GHz, 43 and 40 %: 96 tiles of
+// 29-124 steps for 64 places a KV head end at 148 steps, 123.5 on the average.
 #pragma once
 
 #include <type_traits>

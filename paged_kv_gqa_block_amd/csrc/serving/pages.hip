@@ -16,9 +16,9 @@
 // four a thread) and does 512 tokens or its share of the pages.  Nothing that
 // the others read is written before all are done: the last of several workgroups to
 // finish writes lengths and counts; one workgroup needs nobody.  64 rows of a token each
-// take 4.2 us and give their pages back in 3.5, most of it launch and the chain of loads;
-// 132465 tokens of 256 rows take 9.2 and 6 (7600 pages).  (With the rows scanned again for
-// their results 10.6.)
+// take 4.2-4.6 us and give their pages back in 3.5, most of it launch and the chain of
+// loads; 132465 tokens of 256 rows take 9.2-9.4 and 6.2 (7600 pages).  (With the rows
+// scanned again for their results 10.6.)
 #include "context/states.h"
 #include "context/wave.h"
 #include "serving/serving_internal.h"
@@ -36,7 +36,8 @@ __device__ __forceinline__ int pages_of(int tokens) {
   return (tokens >> 4) + ((tokens & 15) ? 1 : 0);
 }
 
-// Inclusive sum over the wave, no higher than `most` (<= 2^30 + 1).
+// Inclusive sum over the wave, no higher than `most` (below 2^31, so that two such sums add
+// up within 32 bits).
 __device__ __forceinline__ uint32_t capped_scan(uint32_t x, uint32_t most) {
   auto add = [&](int y) { x = min(x + static_cast<uint32_t>(y), most); };
   add(moved<kDppRowShr + 1>(static_cast<int>(x)));

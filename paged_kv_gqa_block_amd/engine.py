@@ -516,7 +516,8 @@ class PromptStep(_ContextCalls):
     `splits`: over 16 and 4 bits the ranges that a tile cuts its keys into at most, over
     8 bits the workgroups of a KV head that its tiles are spread over (pkv_prompt_kv8);
     None: as many as fill the device.  The first call over 8 bits may allocate a
-    workspace: make one before a capture, or the graph clears its own at every call.
+    workspace: make one before a capture, or the graph clears its own at every call, and
+    what is bound in the capture belongs to that graph.
     """
 
     def __init__(self, prob: _lib.pkv_problem, num_tokens: int, window: int = 0, sinks: int = 0,
