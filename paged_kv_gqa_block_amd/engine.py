@@ -565,7 +565,8 @@ class PromptStep(_ContextCalls):
             return self._own
         ws = self._workspace8
         if ws is None:
-            at = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            at = (torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int)
+                  else stream)
             with torch.cuda.device(self.device), torch.cuda.stream(at):
                 if torch.cuda.is_current_stream_capturing():
                     if self._captured8 is None:

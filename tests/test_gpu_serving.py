@@ -751,6 +751,22 @@ def test_workspace_of_shares_first_needed_on_a_busy_stream():
     assert not step._workspace8[:256 << 10].any()
 
 
+@pytest.mark.parametrize("null", [False, True])
+def test_workspace_of_shares_first_needed_on_a_stream_given_by_number(null):
+    b, step = _shares_step()
+    w = b.device()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say("[workspace of shares] stream by number")
+    for number in (0 if null else side.cuda_stream, side.cuda_stream):
+        step.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        out, lse = step.run(w, number)
+        torch.cuda.synchronize()
+        check(out, lse, b.reference(), "f16", 128, b.vmax, True, "shares")
+    assert not step._workspace8[:256 << 10].any()
+
+
 def test_workspace_of_shares_first_needed_in_a_capture():
     """The graph clears the workspace it was captured with; eager calls before and between
     its replays have their own."""
